@@ -30,7 +30,8 @@
  *  - d_* arguments are DEVICE pointers owned by the caller (for instance the
  *    data_ptr() of torch tensors); h_* arguments are HOST pointers.  Nothing
  *    is freed by the library except the opaque handle in lq_state_destroy.
- *  - Floating-point tensors are float32, C-contiguous, in the shapes given.
+ *  - Floating-point tensors are float32, C-contiguous, in the shapes given
+ *    (the recurrent layer's calls take other types and row strides: see there).
  *  - `stream` is a cudaStream_t (NULL = the legacy default stream).  Compute
  *    calls are asynchronous on it unless their comment says they synchronize.
  *  - Every call returns LQ_OK (0) or a negative lq_status; argument errors are
@@ -334,6 +335,139 @@ int lq_prefill(const lq_config *cfg, int32_t T, const float *d_q, const float *d
 int lq_damp_select(const lq_config *cfg, int32_t n_states, const float *d_states,
                    int32_t n_gate_samples, const float *d_gates, double *d_energy,
                    int32_t *d_rows, void *stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The recurrent layer around the state: the short causal convolution ahead of
+ * the recurrence, the selective state-space scan (the sibling recurrence with
+ * one decay per head and no delta term: LinQuant appendix Table 3, Mamba-2
+ * row), and the norms before and after the block -- for prompts and for single
+ * tokens.
+ *
+ * Activations are f32, bf16 or f16 (lq_dtype, one type per call unless stated);
+ * parameters and states are float32.  Sums, decays, norms and states are formed
+ * in FP32 and an output is rounded once.  Arrays of token rows are given by a
+ * base pointer and a row stride in ELEMENTS (ld*, at least the row's width; the
+ * elements of one row are contiguous), so that they may be columns of a wider
+ * projection; bases are aligned to their element.  Rows whose base, stride and
+ * width keep 16-byte alignment take vector accesses; others give the same
+ * results up to rounding order, at a lower rate.
+ *
+ * Prompts: `rows` token rows in all, of B sequences.
+ *   d_cu NULL:  equal lengths T = rows / B (rows divisible by B, else
+ *               LQ_ERR_SHAPE), time-major as in lq_prefill: token t of sequence
+ *               b is row t*B + b.
+ *   d_cu given: packed; sequence b is rows d_cu[b] .. d_cu[b+1] - 1 (int32
+ *               [B+1], DEVICE, non-decreasing, within [0, rows]; checked only
+ *               in that offsets outside are clamped: no access leaves the rows).
+ *               A sequence may be empty: its state passes through.  Rows before
+ *               d_cu[0] and from d_cu[B] on are neither read nor written.
+ * An argument error launches nothing: LQ_ERR_INVALID_ARG (null, misaligned or
+ * overlapping arrays, bad enum), LQ_ERR_SHAPE (sizes or strides inconsistent),
+ * LQ_ERR_UNSUPPORTED (size not built).  All calls are asynchronous on `stream`,
+ * allocate nothing and may be captured into a graph.
+ * ---------------------------------------------------------------------------
+ */
+typedef enum { LQ_F32 = 0, LQ_BF16 = 1, LQ_F16 = 2 } lq_dtype;
+typedef enum { LQ_ACT_NONE = 0, LQ_ACT_SILU = 1, LQ_ACT_SIGMOID = 2 } lq_act;
+
+/* Taps of the convolution: 2 .. LQ_CONV_MAX_TAPS. */
+#define LQ_CONV_MAX_TAPS 4
+
+typedef struct {
+    int32_t dtype;   /* lq_dtype of x, y and the window */
+    int32_t B;       /* sequences */
+    int32_t C;       /* channels */
+    int32_t K;       /* taps */
+    int32_t act;     /* LQ_ACT_NONE or LQ_ACT_SILU */
+} lq_conv_config;
+
+/*
+ * Short causal depthwise convolution over prompts:
+ *   y_t[c] = act(bias[c] + sum_{j<K} w[c,j] x_{t-K+1+j}[c])
+ *   d_x [rows,C], d_w [C,K], d_bias [C] or NULL -> d_y [rows,C]
+ * Inputs before a sequence's first token come from its window d_state0
+ * [B,K-1,C] (oldest first; NULL = zeros).  d_state_out [B,K-1,C] (NULL: not
+ * written; may be d_state0) receives the last K-1 inputs -- the window's own
+ * rows where the sequence is shorter.  d_y must not overlap d_x.
+ */
+int lq_conv_prefill(const lq_conv_config *cfg, int32_t rows, const int32_t *d_cu, const void *d_x, int64_t ldx,
+                    const float *d_w, const float *d_bias, const void *d_state0, void *d_state_out, void *d_y,
+                    int64_t ldy, void *stream);
+
+/* The same for one token of each sequence, d_x [B,C] -> d_y [B,C] (may be d_x);
+ * the windows d_state [B,K-1,C] are shifted in place. */
+int lq_conv_step(const lq_conv_config *cfg, void *d_state, const void *d_x, int64_t ldx, const float *d_w,
+                 const float *d_bias, void *d_y, int64_t ldy, void *stream);
+
+typedef struct {
+    int32_t dtype;      /* lq_dtype of x, dt, Bm, Cm and y */
+    int32_t B, H, G;    /* sequences, heads, groups of Bm / Cm (G divides H; head h reads group h*G/H) */
+    int32_t dk, dv;     /* state rows (Bm, Cm) and columns (x): 64 or 128 each */
+    int32_t softplus;   /* 1: d_t = log(1 + exp(dt_t + dt_bias)); 0: d_t = dt_t + dt_bias */
+} lq_ssm_config;
+
+/* Bytes of device workspace lq_ssm_prefill needs for `rows` rows (0 if none is
+ * needed or cfg is invalid). */
+size_t lq_ssm_workspace_bytes(const lq_ssm_config *cfg, int32_t rows);
+
+/*
+ * Selective state-space scan over prompts, per head (the state S is dk x dv, as
+ * everywhere in this library):
+ *   S_t = a_t S_{t-1} + d_t B_t x_t^T,   a_t = exp(d_t A_h),   y_t = S_t^T C_t + D_h x_t
+ *   d_x [rows,H,dv], d_dt [rows,H], d_Bm, d_Cm [rows,G,dk], d_A [H] (at most 0 for a
+ *   decaying state), d_D [H] or NULL (0), d_dt_bias [H] or NULL (0)
+ *   -> d_y [rows,H,dv] and the final states d_S_out [B,H,dk,dv], from d_S0 [B,H,dk,dv]
+ *   (NULL = zeros; d_S_out may be d_S0).
+ * Long prompts run in chunks whose products use the tensor cores with FP32-level
+ * accuracy; one step's log decay d_t A_h is floored at -104 there (2^-150: a
+ * factor that FP32 flushes to 0).  d_ws: caller-owned device workspace of at
+ * least lq_ssm_workspace_bytes(cfg, rows) bytes, 256-byte aligned (else
+ * LQ_ERR_WORKSPACE; NULL when that is 0), used by this call until it completes
+ * on `stream`: calls that may overlap need a workspace each, graphs that may
+ * run at the same time included.  d_y must not overlap an input.
+ */
+int lq_ssm_prefill(const lq_ssm_config *cfg, int32_t rows, const int32_t *d_cu, const void *d_x, int64_t ldx,
+                   const void *d_dt, int64_t lddt, const float *d_A, const void *d_Bm, int64_t ldb, const void *d_Cm,
+                   int64_t ldc, const float *d_D, const float *d_dt_bias, const float *d_S0, float *d_S_out, void *d_y,
+                   int64_t ldy, void *d_ws, size_t ws_bytes, void *stream);
+
+/* The same for one token of each sequence (rows [B, ...]); the states d_S
+ * [B,H,dk,dv] are updated in place.  No workspace. */
+int lq_ssm_step(const lq_ssm_config *cfg, float *d_S, const void *d_x, int64_t ldx, const void *d_dt, int64_t lddt,
+                const float *d_A, const void *d_Bm, int64_t ldb, const void *d_Cm, int64_t ldc, const float *d_D,
+                const float *d_dt_bias, void *d_y, int64_t ldy, void *stream);
+
+/* Longest group a norm takes its statistic over. */
+#define LQ_NORM_MAX_D 16384
+
+typedef struct {
+    int32_t dtype;       /* lq_dtype of z, res, h and y */
+    int32_t x_dtype;     /* lq_dtype of x: dtype, or LQ_F32 in lq_norm_out (a decode step's outputs) */
+    int32_t rows;
+    int32_t G, D;        /* groups per row and elements per group (lq_norm_in: G = 1) */
+    int32_t w_groups;    /* 1: weights [G,D]; 0: [D], shared by the groups */
+    int32_t act;         /* lq_norm_out's gate: LQ_ACT_SILU or LQ_ACT_SIGMOID */
+    int32_t gate_first;  /* 1: the gate is applied before the norm, 0: after */
+    float eps;           /* > 0 */
+    float scale;         /* residual scale, times d_scale where given */
+} lq_norm_config;
+
+/*
+ * Norms of the layer, rms(u) = u / sqrt(mean u^2 + eps) over each group of D.
+ * lq_norm_in, before a block: d_h = d_res + scale d_x (the residual stream, d_res
+ * NULL = 0; d_h NULL = not written), d_y = rms(h) w of the unrounded sum.
+ * lq_norm_out, after a block: d_y = d_res + scale (rms(x) w act(z)), gate first:
+ * d_y = d_res + scale (rms(x act(z)) w); d_z NULL = no gate, d_res NULL = 0.
+ * d_scale [G*D] float32 or NULL: a scale per channel.  d_y and d_h may each be one of the
+ * inputs of the same type and stride; otherwise nothing may overlap them.
+ * The L2 norm of q and k ahead of a delta-rule recurrence is lq_norm_out with
+ * weights 1 / sqrt(D): x / sqrt(sum x^2 + D eps).
+ */
+int lq_norm_in(const lq_norm_config *cfg, const void *d_x, int64_t ldx, const float *d_w, const void *d_res,
+               int64_t ldres, const float *d_scale, void *d_h, int64_t ldh, void *d_y, int64_t ldy, void *stream);
+int lq_norm_out(const lq_norm_config *cfg, const void *d_x, int64_t ldx, const float *d_w, const void *d_z, int64_t ldz,
+                const void *d_res, int64_t ldres, const float *d_scale, void *d_y, int64_t ldy, void *stream);
 
 /*
  * Self-test of the library's internal division (no counterpart in the papers:

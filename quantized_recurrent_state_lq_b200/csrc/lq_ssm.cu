@@ -1,0 +1,126 @@
+// lq_ssm.cu -- the selective state-space scan, token by token:
+//   d_t = softplus(dt_t + bias) (or dt_t),  a_t = exp(d_t A_h),
+//   S_t = a_t S_{t-1} + d_t B_t x_t^T,      y_t = S_t^T C_t + D_h x_t
+// for states S [dk][dv] of every head (key rows, value columns); head h reads
+// group h * G / H of B and C.
+//
+// ssm_step_kernel: bound by HBM, the state is read and written once (8 dk dv
+// bytes per head against 5 dk dv flops).  The state's value columns are
+// independent, so a CTA takes CW columns of a head: 64 when the heads fill
+// the GPU (16 16-byte loads in flight per thread), 16 when they do not (four
+// times the CTAs, a quarter of the serial work each).  The state stays in
+// registers over the tokens of a short prompt.
+#include "lq_act.cuh"
+
+namespace lq {
+namespace {
+
+constexpr int kStepThreads = 128;
+
+template <typename T, int DK, int DV, int CW>
+__global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(SsmArgs a) {
+    constexpr int LR = CW / 4;               // lanes per key row
+    constexpr int RG = kStepThreads / LR;    // key rows side by side
+    constexpr int NR = DK / RG;              // key rows per thread
+    __shared__ float sB[DK], sC[DK], sx[CW], part[kStepThreads / 32][CW];
+    const int tid = threadIdx.x;
+    const int slice = blockIdx.x % (DV / CW);
+    const int64_t bh = blockIdx.x / (DV / CW);
+    const int b = (int)(bh / a.H), h = (int)(bh - (int64_t)b * a.H);
+    const int g = (int)((int64_t)h * a.G / a.H);
+    Piece p;
+    p.row0 = b;
+    p.step = a.r.B;
+    p.len = a.r.rows / a.r.B;
+    if (a.r.cu) {
+        const int c0 = cu_at(a.r, b);
+        p.row0 = c0;
+        p.step = 1;
+        p.len = max(cu_at(a.r, b + 1), c0) - c0;
+    }
+    const int col = 4 * (tid % LR), rg = tid / LR;
+    const int64_t base = bh * DK * DV + slice * CW + col;
+    float4 S[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+        S[i] = a.S0 ? *reinterpret_cast<const float4 *>(a.S0 + base + (int64_t)(rg + i * RG) * DV)
+                    : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float A = a.A[h], Dh = a.D ? a.D[h] : 0.0f, bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
+    for (int t = 0; t < p.len; ++t) {
+        const int64_t row = p.row0 + t * p.step;
+        const T *Bm = static_cast<const T *>(a.Bm) + row * a.ldb + g * DK;
+        const T *Cm = static_cast<const T *>(a.Cm) + row * a.ldc + g * DK;
+        if (tid < DK) {
+            sB[tid] = to_f<T>(Bm[tid]);
+            sC[tid] = to_f<T>(Cm[tid]);
+        }
+        if (tid < CW) sx[tid] = to_f<T>(static_cast<const T *>(a.x)[row * a.ldx + (int64_t)h * DV + slice * CW + tid]);
+        float d = to_f<T>(static_cast<const T *>(a.dt)[row * a.lddt + h]) + bias;
+        if (a.softplus) d = softplus_f(d);
+        const float keep = expf(d * A);
+        __syncthreads();
+        const float4 x = *reinterpret_cast<const float4 *>(sx + col);
+        const float4 dx = make_float4(d * x.x, d * x.y, d * x.z, d * x.w);
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            const float bn = sB[rg + i * RG], cn = sC[rg + i * RG];
+            S[i].x = fmaf(bn, dx.x, keep * S[i].x);
+            S[i].y = fmaf(bn, dx.y, keep * S[i].y);
+            S[i].z = fmaf(bn, dx.z, keep * S[i].z);
+            S[i].w = fmaf(bn, dx.w, keep * S[i].w);
+            y.x = fmaf(cn, S[i].x, y.x);
+            y.y = fmaf(cn, S[i].y, y.y);
+            y.z = fmaf(cn, S[i].z, y.z);
+            y.w = fmaf(cn, S[i].w, y.w);
+        }
+#pragma unroll
+        for (int m = LR; m < 32; m <<= 1) {
+            y.x += __shfl_xor_sync(0xffffffffu, y.x, m);
+            y.y += __shfl_xor_sync(0xffffffffu, y.y, m);
+            y.z += __shfl_xor_sync(0xffffffffu, y.z, m);
+            y.w += __shfl_xor_sync(0xffffffffu, y.w, m);
+        }
+        if ((tid & 31) < LR) *reinterpret_cast<float4 *>(&part[tid >> 5][col]) = y;
+        __syncthreads();
+        if (tid < CW) {
+            float s = Dh * sx[tid];
+#pragma unroll
+            for (int w = 0; w < kStepThreads / 32; ++w) s += part[w][tid];
+            static_cast<T *>(a.y)[row * a.ldy + (int64_t)h * DV + slice * CW + tid] = from_f<T>(s);
+        }
+        if (t + 1 < p.len) __syncthreads();   // sx and part are read before the next token's are written
+    }
+#pragma unroll
+    for (int i = 0; i < NR; ++i) *reinterpret_cast<float4 *>(a.S_out + base + (int64_t)(rg + i * RG) * DV) = S[i];
+}
+
+template <typename T, int DK, int DV>
+cudaError_t step(const SsmArgs &a, cudaStream_t s) {
+    const int64_t heads = (int64_t)a.r.B * a.H;
+    if (heads * (DV / 64) >= 148 * 2)
+        ssm_step_kernel<T, DK, DV, 64><<<(unsigned)(heads * (DV / 64)), kStepThreads, 0, s>>>(a);
+    else
+        ssm_step_kernel<T, DK, DV, 16><<<(unsigned)(heads * (DV / 16)), kStepThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t step_sizes(const SsmArgs &a, cudaStream_t s) {
+    if (a.dk == 64) return a.dv == 64 ? step<T, 64, 64>(a, s) : step<T, 64, 128>(a, s);
+    return a.dv == 64 ? step<T, 128, 64>(a, s) : step<T, 128, 128>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_ssm_step(const SsmArgs &a, int dtype, cudaStream_t s) {
+    if (dtype == kF32) return step_sizes<float>(a, s);
+    if (dtype == kBF16) return step_sizes<bf16>(a, s);
+    return step_sizes<f16>(a, s);
+}
+
+size_t ssm_ws_bytes(int, int, int, int, int, int, int) { return 0; }
+
+cudaError_t launch_ssm_prefill(const SsmArgs &a, int dtype, cudaStream_t s) { return launch_ssm_step(a, dtype, s); }
+
+}  // namespace lq

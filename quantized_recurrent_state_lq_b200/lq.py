@@ -34,7 +34,9 @@ EXPORTED = ["lq_workspace_bytes", "lq_config_check", "lq_state_init", "lq_decode
             "lq_state_export_view", "lq_state_import_view", "lq_quantize_state",
             "lq_dequantize_state", "lq_quantize_state_static", "lq_damp_select", "lq_get_status",
             "lq_state_destroy", "lq_strerror", "lq_selftest_division", "lq_prefill",
-            "lq_state_init_static", "lq_fit_static_scales", "lq_selftest_wait", "lq_state_set_phases"]
+            "lq_state_init_static", "lq_fit_static_scales", "lq_selftest_wait", "lq_state_set_phases",
+            "lq_conv_prefill", "lq_conv_step", "lq_ssm_workspace_bytes", "lq_ssm_prefill", "lq_ssm_step",
+            "lq_norm_in", "lq_norm_out"]
 
 
 class LqError(RuntimeError):
@@ -47,6 +49,19 @@ class lq_config(C.Structure):
     _fields_ = [(n, C.c_int32) for n in ("B", "H", "Hk", "dk", "dv", "gate", "mode", "W", "r",
                                           "power_iters", "n_hp_rows", "smoothing", "fused_flush",
                                           "buffer_bf16", "state_bits")]
+
+
+class lq_conv_config(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("dtype", "B", "C", "K", "act")]
+
+
+class lq_ssm_config(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("dtype", "B", "H", "G", "dk", "dv", "softplus")]
+
+
+class lq_norm_config(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("dtype", "x_dtype", "rows", "G", "D", "w_groups", "act",
+                                          "gate_first")] + [("eps", C.c_float), ("scale", C.c_float)]
 
 
 class lq_qstate_view(C.Structure):
@@ -65,7 +80,7 @@ def lib():
         if not os.path.exists(LIB_PATH) or _build._stale():
             _build.build()
         L = C.CDLL(LIB_PATH)
-        vp, i32, sz = C.c_void_p, C.c_int32, C.c_size_t
+        vp, i32, i64, sz = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t
         cfgp = C.POINTER(lq_config)
         viewp = C.POINTER(lq_qstate_view)
         sig = {
@@ -91,6 +106,14 @@ def lib():
             "lq_fit_static_scales": (C.c_int, [cfgp, i32, vp, i32, vp, vp, vp, vp]),
             "lq_selftest_wait": (C.c_int, [vp, C.c_int64, vp]),
             "lq_state_set_phases": (C.c_int, [vp, vp, vp]),
+            "lq_conv_prefill": (C.c_int, [vp, i32, vp, vp, i64, vp, vp, vp, vp, vp, i64, vp]),
+            "lq_conv_step": (C.c_int, [vp, vp, vp, i64, vp, vp, vp, i64, vp]),
+            "lq_ssm_workspace_bytes": (sz, [vp, i32]),
+            "lq_ssm_prefill": (C.c_int, [vp, i32, vp, vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, vp, vp, vp, vp, i64,
+                                         vp, sz, vp]),
+            "lq_ssm_step": (C.c_int, [vp, vp, vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, vp, vp, i64, vp]),
+            "lq_norm_in": (C.c_int, [vp, vp, i64, vp, vp, i64, vp, vp, i64, vp, i64, vp]),
+            "lq_norm_out": (C.c_int, [vp, vp, i64, vp, vp, i64, vp, i64, vp, vp, i64, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -411,3 +434,276 @@ def lq_state_destroy(st: LqState):
     if st.handle.value:
         lib().lq_state_destroy(st.handle)
         st.handle = C.c_void_p(0)
+
+
+# ---------------------------------------------------------------------------
+# The recurrent layer around the state: short causal convolution, selective
+# state-space scan, norms.  Activations float32, bfloat16 or float16; prompts
+# are packed ([rows, ...] with cu, the B+1 int32 row offsets on the device) or
+# time-major ([T, B, ...]); rows may be columns of a wider tensor.
+# ---------------------------------------------------------------------------
+LQ_F32, LQ_BF16, LQ_F16 = 0, 1, 2
+LQ_ACT_NONE, LQ_ACT_SILU, LQ_ACT_SIGMOID = 0, 1, 2
+LQ_CONV_MAX_TAPS = 4
+LQ_NORM_MAX_D = 16384
+
+_DTYPES = {torch.float32: LQ_F32, torch.bfloat16: LQ_BF16, torch.float16: LQ_F16}
+_ACTS = {None: LQ_ACT_NONE, "silu": LQ_ACT_SILU, "sigmoid": LQ_ACT_SIGMOID}
+
+
+class _On:
+    """The device of a call's tensors and the stream it runs on: torch's current
+    stream of that device, or the one given.  Inside, both are current, so what
+    the call allocates belongs to the stream it is used on."""
+
+    def __init__(self, t: torch.Tensor, stream=None):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError("the inputs must be CUDA tensors")
+        self.device = t.device
+        self.guard = None
+        if stream is not None:
+            if stream.device != t.device:
+                raise ValueError(f"stream of {stream.device} for tensors on {t.device}")
+            self.guard = torch.cuda.stream(stream)
+        elif t.device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(t.device)
+        self.given = stream is not None
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        self.stream = torch.cuda.current_stream(self.device).cuda_stream
+        return self
+
+    def __exit__(self, *e):
+        if self.guard is not None:
+            self.guard.__exit__(*e)
+
+    def _have(self, t, name, dtype):
+        if not isinstance(t, torch.Tensor) or t.device != self.device:
+            raise TypeError(f"{name} must be a CUDA tensor on {self.device}")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if self.given:          # its memory is not reused before this stream is done with it
+            t.record_stream(torch.cuda.current_stream(self.device))
+
+    def rows(self, t, name, shape, n_tail, dtype):
+        """Pointer and row stride of a tensor of token rows: its last n_tail
+        dimensions are one contiguous row, the others evenly spaced rows."""
+        self._have(t, name, dtype)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+        st = t.stride()
+        w = 1
+        for i in range(len(shape) - 1, len(shape) - 1 - n_tail, -1):
+            if shape[i] != 1 and st[i] != w:
+                raise ValueError(f"{name}: the elements of a row must be contiguous")
+            w *= shape[i]
+        ld, n = w, 1
+        for i in range(len(shape) - n_tail - 1, -1, -1):
+            if shape[i] != 1:
+                if n == 1:
+                    ld = st[i]
+                elif st[i] != n * ld:
+                    raise ValueError(f"{name}: rows must be evenly spaced")
+                n *= shape[i]
+        return t.data_ptr(), ld
+
+    def flat(self, t, name, shape, dtype=torch.float32):
+        """Pointer of an optional contiguous tensor."""
+        if t is None:
+            return None
+        self._have(t, name, dtype)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr()
+
+    def new(self, shape, dtype):
+        return torch.empty(shape, dtype=dtype, device=self.device)
+
+
+def _dtype_of(t: torch.Tensor) -> int:
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"activations must be float32, bfloat16 or float16, got {t.dtype}")
+    return _DTYPES[t.dtype]
+
+
+def _act_of(act) -> int:
+    if act not in _ACTS:
+        raise ValueError(f"unknown activation {act!r}")
+    return _ACTS[act]
+
+
+def _prompt(x: torch.Tensor, cu, n_tail: int, on: _On):
+    """(B, rows, pointer of cu or None) of a packed or time-major prompt batch."""
+    lead = x.shape[:x.dim() - n_tail]
+    if cu is None:
+        if len(lead) != 2:
+            raise ValueError(f"a time-major prompt is [T, B, ...], got {tuple(x.shape)}; a packed one needs cu")
+        return lead[1], lead[0] * lead[1], None
+    if len(lead) != 1:
+        raise ValueError(f"a packed prompt is [rows, ...], got {tuple(x.shape)}")
+    if cu.dim() != 1 or cu.shape[0] < 2:
+        raise ValueError("cu must hold B+1 offsets")
+    return cu.shape[0] - 1, lead[0], on.flat(cu, "cu", (cu.shape[0],), torch.int32)
+
+
+def lq_conv_prefill(x, w, bias=None, act="silu", state0=None, state_out=None, y=None, cu=None, stream=None):
+    """Short causal depthwise convolution over prompts x ([rows, C] with cu, or
+    [T, B, C]) with taps w [C, K], from the windows state0 [B, K-1, C] (None:
+    zeros).  Returns (y, state_out), allocated when None; state_out may be
+    state0."""
+    with _On(x, stream) as on:
+        dt = x.dtype
+        code = _dtype_of(x)
+        B, rows, p_cu = _prompt(x, cu, 1, on)
+        ch, K = w.shape
+        lead = tuple(x.shape[:-1])
+        px, ldx = on.rows(x, "x", (*lead, ch), 1, dt)
+        y = on.new((*lead, ch), dt) if y is None else y
+        py, ldy = on.rows(y, "y", (*lead, ch), 1, dt)
+        win = (B, K - 1, ch)
+        state_out = on.new(win, dt) if state_out is None else state_out
+        cfg = lq_conv_config(code, B, ch, K, _act_of(act))
+        _chk(lib().lq_conv_prefill(C.addressof(cfg), rows, p_cu, px, ldx, on.flat(w, "w", (ch, K)),
+                                   on.flat(bias, "bias", (ch,)), on.flat(state0, "state0", win, dt),
+                                   on.flat(state_out, "state_out", win, dt), py, ldy, on.stream), "lq_conv_prefill")
+    return y, state_out
+
+
+def lq_conv_step(state, x, w, bias=None, act="silu", y=None, stream=None):
+    """One token of every sequence, x [B, C]; the windows state [B, K-1, C] move
+    on in place.  Returns y [B, C] (allocated when None; may be x)."""
+    with _On(x, stream) as on:
+        dt = x.dtype
+        code = _dtype_of(x)
+        ch, K = w.shape
+        B = x.shape[0]
+        px, ldx = on.rows(x, "x", (B, ch), 1, dt)
+        y = on.new((B, ch), dt) if y is None else y
+        py, ldy = on.rows(y, "y", (B, ch), 1, dt)
+        cfg = lq_conv_config(code, B, ch, K, _act_of(act))
+        _chk(lib().lq_conv_step(C.addressof(cfg), on.flat(state, "state", (B, K - 1, ch), dt), px, ldx,
+                                on.flat(w, "w", (ch, K)), on.flat(bias, "bias", (ch,)), py, ldy, on.stream),
+             "lq_conv_step")
+    return y
+
+
+def lq_ssm_workspace_bytes(dtype, B: int, H: int, G: int, dk: int, dv: int, rows: int) -> int:
+    """Bytes of the workspace lq_ssm_prefill takes for these sizes."""
+    cfg = lq_ssm_config(_DTYPES[dtype], B, H, G, dk, dv, 1)
+    return lib().lq_ssm_workspace_bytes(C.addressof(cfg), rows)
+
+
+def lq_ssm_prefill(x, dt, A, Bm, Cm, D=None, dt_bias=None, softplus=True, S0=None, S_out=None, y=None, cu=None,
+                   workspace=None, stream=None):
+    """Selective state-space scan over prompts: x [..., H, dv], dt [..., H],
+    Bm, Cm [..., G, dk] with [...] = [rows] (and cu) or [T, B]; A, D, dt_bias
+    [H].  From the states S0 [B, H, dk, dv] (None: zeros).  Returns
+    (y [..., H, dv], S_out), allocated when None; S_out may be S0.  The
+    workspace (uint8, at least lq_ssm_workspace_bytes) is allocated when None."""
+    with _On(x, stream) as on:
+        t = x.dtype
+        code = _dtype_of(x)
+        B, rows, p_cu = _prompt(x, cu, 2, on)
+        lead, (H, dv), (G, dk) = tuple(x.shape[:-2]), x.shape[-2:], Bm.shape[-2:]
+        px, ldx = on.rows(x, "x", (*lead, H, dv), 2, t)
+        pd, ldd = on.rows(dt, "dt", (*lead, H), 1, t)
+        pb, ldb = on.rows(Bm, "Bm", (*lead, G, dk), 2, t)
+        pc, ldc = on.rows(Cm, "Cm", (*lead, G, dk), 2, t)
+        y = on.new((*lead, H, dv), t) if y is None else y
+        py, ldy = on.rows(y, "y", (*lead, H, dv), 2, t)
+        st = (B, H, dk, dv)
+        S_out = on.new(st, torch.float32) if S_out is None else S_out
+        cfg = lq_ssm_config(code, B, H, G, dk, dv, int(bool(softplus)))
+        need = lib().lq_ssm_workspace_bytes(C.addressof(cfg), rows)
+        if workspace is None and need:
+            workspace = on.new((need,), torch.uint8)
+        p_ws, n_ws = None, 0
+        if workspace is not None:
+            n_ws = workspace.numel()
+            p_ws = on.flat(workspace, "workspace", (n_ws,), torch.uint8)
+        _chk(lib().lq_ssm_prefill(C.addressof(cfg), rows, p_cu, px, ldx, pd, ldd, on.flat(A, "A", (H,)), pb, ldb, pc,
+                                  ldc, on.flat(D, "D", (H,)), on.flat(dt_bias, "dt_bias", (H,)),
+                                  on.flat(S0, "S0", st), on.flat(S_out, "S_out", st), py, ldy, p_ws, n_ws, on.stream),
+             "lq_ssm_prefill")
+    return y, S_out
+
+
+def lq_ssm_step(S, x, dt, A, Bm, Cm, D=None, dt_bias=None, softplus=True, y=None, stream=None):
+    """One token of every sequence: x [B, H, dv], dt [B, H], Bm, Cm [B, G, dk];
+    the states S [B, H, dk, dv] are updated in place.  Returns y [B, H, dv]
+    (allocated when None)."""
+    with _On(x, stream) as on:
+        t = x.dtype
+        code = _dtype_of(x)
+        (B, H, dv), (G, dk) = x.shape, Bm.shape[-2:]
+        px, ldx = on.rows(x, "x", (B, H, dv), 2, t)
+        pd, ldd = on.rows(dt, "dt", (B, H), 1, t)
+        pb, ldb = on.rows(Bm, "Bm", (B, G, dk), 2, t)
+        pc, ldc = on.rows(Cm, "Cm", (B, G, dk), 2, t)
+        y = on.new((B, H, dv), t) if y is None else y
+        py, ldy = on.rows(y, "y", (B, H, dv), 2, t)
+        cfg = lq_ssm_config(code, B, H, G, dk, dv, int(bool(softplus)))
+        _chk(lib().lq_ssm_step(C.addressof(cfg), on.flat(S, "S", (B, H, dk, dv)), px, ldx, pd, ldd,
+                               on.flat(A, "A", (H,)), pb, ldb, pc, ldc, on.flat(D, "D", (H,)),
+                               on.flat(dt_bias, "dt_bias", (H,)), py, ldy, on.stream), "lq_ssm_step")
+    return y
+
+
+def _scale(scale, on: _On, shape):
+    """(factor, pointer of the per-channel scale) of a number or a tensor."""
+    if isinstance(scale, torch.Tensor):
+        return 1.0, on.flat(scale, "scale", shape)
+    return float(scale), None
+
+
+def lq_norm_in(x, w, res=None, scale=1.0, eps=1e-5, h=None, y=None, stream=None):
+    """Norm before a block, with the residual: h = res + scale x, y = rms(h) w
+    over the last dimension of x [..., D]; scale is a number or a float32 tensor
+    [D].  Returns (y, h), allocated when None; h and y may be x or res."""
+    with _On(x, stream) as on:
+        t = x.dtype
+        code = _dtype_of(x)
+        shape = tuple(x.shape)
+        D = shape[-1]
+        px, ldx = on.rows(x, "x", shape, 1, t)
+        pr, ldr = on.rows(res, "res", shape, 1, t) if res is not None else (None, 0)
+        h = on.new(shape, t) if h is None else h
+        y = on.new(shape, t) if y is None else y
+        ph, ldh = on.rows(h, "h", shape, 1, t)
+        py, ldy = on.rows(y, "y", shape, 1, t)
+        s, ps = _scale(scale, on, (D,))
+        cfg = lq_norm_config(code, code, x.numel() // max(D, 1), 1, D, 0, 0, 0, eps, s)
+        _chk(lib().lq_norm_in(C.addressof(cfg), px, ldx, on.flat(w, "w", (D,)), pr, ldr, ps, ph, ldh, py, ldy,
+                              on.stream), "lq_norm_in")
+    return y, h
+
+
+def lq_norm_out(x, w, z=None, act="silu", gate_first=False, res=None, scale=1.0, eps=1e-5, y=None, stream=None):
+    """Norm after a block, with its gate and the residual, over the last
+    dimension of x [..., G, D] (x may be float32 beside 16-bit z, res and y):
+    y = res + scale (rms(x) w act(z)), gate_first: res + scale (rms(x act(z)) w).
+    w is [D] or [G, D]; scale a number or a float32 tensor [G, D].  The type of
+    y is that of z, res or a given y, else x's.  Returns y."""
+    with _On(x, stream) as on:
+        t = next((v.dtype for v in (y, z, res) if v is not None), x.dtype)
+        shape = tuple(x.shape)
+        if len(shape) < 2:
+            raise ValueError(f"x is [..., G, D], got {shape}")
+        G, D = shape[-2:]
+        xcode = _dtype_of(x)
+        px, ldx = on.rows(x, "x", shape, 2, x.dtype)
+        pz, ldz = on.rows(z, "z", shape, 2, t) if z is not None else (None, 0)
+        pr, ldr = on.rows(res, "res", shape, 2, t) if res is not None else (None, 0)
+        y = on.new(shape, t) if y is None else y
+        py, ldy = on.rows(y, "y", shape, 2, t)
+        wg = w.dim() == 2
+        pw = on.flat(w, "w", (G, D) if wg else (D,))
+        s, ps = _scale(scale, on, (G, D))
+        cfg = lq_norm_config(_dtype_of(y), xcode, x.numel() // max(G * D, 1), G, D, int(wg), _act_of(act),
+                             int(bool(gate_first)), eps, s)
+        _chk(lib().lq_norm_out(C.addressof(cfg), px, ldx, pw, pz, ldz, pr, ldr, ps, py, ldy, on.stream), "lq_norm_out")
+    return y

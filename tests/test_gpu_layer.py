@@ -1,0 +1,427 @@
+"""GPU parity of the recurrent layer's operators (convolution, selective scan,
+norms) against their definitions in 64 bits.
+
+Tolerances, per element: one rounding to the output's type (half a step of its
+value) plus the FP32 error of the sum behind it, a multiple of 2^-24 times the
+sum of the magnitudes of its terms:
+  conv   K + 1 roundings of the products and sums;
+  scan   every term passes at most n = T decays, each rounded twice and with an
+         exponential good to a few ulps: Higham and Mary's probabilistic bound
+         lambda sqrt(n) u per path (lambda = 8) with 3 roundings a step, plus
+         the split products of the chunk form (2^-21 of a term) and dk-term sums;
+  norm   sqrt(D) of the statistic (probabilistic) and a few roundings.
+SiLU and sigmoid take the hardware exponential for 16-bit outputs: 2^-18
+relative for the arguments drawn here (|v| < 30: the argument's rounding moves
+the exponential by |v| 2^-23), and at f32 the library's (2^-21)."""
+import math
+
+import pytest
+import torch
+
+from quantized_recurrent_state_lq_b200 import lq
+from tests import layer_ref as R
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
+TYPES = [F32, BF16, F16]
+ids = lambda v: str(v).replace("torch.", "")   # noqa: E731
+
+
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _randn(g, shape, dtype=F32, scale=1.0):
+    return (torch.randn(shape, generator=g, device="cuda") * scale).to(dtype)
+
+
+def _cu(lens):
+    at = [0]
+    for n in lens:
+        at.append(at[-1] + n)
+    return torch.tensor(at, dtype=torch.int32, device="cuda")
+
+
+def _close(got, want, tol, what):
+    assert got.shape == want.shape, what
+    assert torch.isfinite(got).all(), f"{what}: not finite"
+    off = (got.double() - want).abs() / tol
+    worst = off.max().item() if off.numel() else 0.0
+    print(f"{what}: {worst:.3f} of the tolerance")
+    assert worst <= 1.0, f"{what}: {worst:.3g} times the tolerance at {int(off.argmax())}"
+
+
+def _act_rel(dtype, act):
+    return 0.0 if act is None else (2.0 ** -21 if dtype == F32 else 2.0 ** -18)
+
+
+# -- convolution ------------------------------------------------------------------
+
+def _conv_tol(y, mag, dtype, K, act):
+    # |silu'| <= 1.1: the sum's error passes through
+    return (R.half_step(dtype) * (1 + 1e-3) + _act_rel(dtype, act)) * y.abs() + 1.1 * (K + 2) * R.U * mag + R.tiny(dtype)
+
+
+def _check_conv(x, w, bias, act, state, cu, what):
+    y, win = lq.lq_conv_prefill(x, w, bias, act=act, state0=state, cu=cu)
+    ry, rw, mag = R.conv(x, w, bias, act, state, cu)
+    _close(y, ry, _conv_tol(ry, mag, x.dtype, w.shape[1], act), what)
+    assert torch.equal(win.double(), rw), f"{what}: window"
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("K", [2, 3, 4])
+@pytest.mark.parametrize("C", [1, 37, 64, 1030, 2304])
+def test_conv_packed(dtype, K, C):
+    """Sequences of 0, 1, 2, 3 tokens and around the pieces' ends, windows given."""
+    _gpu()
+    g = _gen(C * 10 + K)
+    cu = _cu([0, 1, 2, 3, 64, 0, 65, 63, 130, 1])
+    n = int(cu[-1])
+    x = _randn(g, (n, C + 24), dtype)[:, 8:8 + C]          # columns of a wider tensor
+    w, bias = _randn(g, (C, K)), _randn(g, (C,))
+    state = _randn(g, (10, K - 1, C), dtype)
+    _check_conv(x, w, bias, "silu", state, cu, f"conv {ids(dtype)} K{K} C{C}")
+    _check_conv(x, w, None, None, None, cu, f"conv plain {ids(dtype)} K{K} C{C}")
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("T", [0, 1, 2, 3, 64, 100])
+def test_conv_time_major(dtype, T):
+    _gpu()
+    g = _gen(T)
+    x, w, bias = _randn(g, (T, 3, 80), dtype), _randn(g, (80, 4)), _randn(g, (80,))
+    state = _randn(g, (3, 3, 80), dtype)
+    _check_conv(x, w, bias, "silu", state, None, f"conv time-major {ids(dtype)} T{T}")
+
+
+def test_conv_in_place_window_and_pieces_match_one_call():
+    """Two calls with the window carried in place equal one call, bit for bit."""
+    _gpu()
+    g = _gen(5)
+    x, w, bias = _randn(g, (150, 2, 96), BF16), _randn(g, (96, 4)), _randn(g, (96,))
+    state = _randn(g, (2, 3, 96), BF16)
+    one, last = lq.lq_conv_prefill(x, w, bias, state0=state)
+    s = state.clone()
+    got = []
+    for a, b in ((0, 1), (1, 3), (3, 70), (70, 150)):
+        y, _ = lq.lq_conv_prefill(x[a:b], w, bias, state0=s, state_out=s)
+        got.append(y)
+    assert torch.equal(torch.cat(got), one) and torch.equal(s, last)
+    s = state.clone()
+    for t in range(150):
+        assert torch.equal(lq.lq_conv_step(s, x[t], w, bias), one[t]), t
+    assert torch.equal(s, last)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("B,C,K", [(1, 2304, 4), (3, 37, 2), (130, 200, 3)])
+def test_conv_step(dtype, B, C, K):
+    _gpu()
+    g = _gen(B)
+    x = _randn(g, (B, C + 8), dtype)[:, :C]
+    w, bias, state = _randn(g, (C, K)), _randn(g, (C,)), _randn(g, (B, K - 1, C), dtype)
+    ry, rw, mag = R.conv(x[None], w, bias, "silu", state, None)
+    y = lq.lq_conv_step(state, x, w, bias)
+    _close(y, ry[0], _conv_tol(ry[0], mag[0], dtype, K, "silu"), f"conv step {ids(dtype)}")
+    assert torch.equal(state.double(), rw)
+
+
+def test_conv_rows_outside_the_sequences_stay():
+    """Rows before cu[0] and from cu[B] on are not written."""
+    _gpu()
+    g = _gen(1)
+    x, w = _randn(g, (40, 64), BF16), _randn(g, (64, 4))
+    cu = torch.tensor([5, 9, 9, 30], dtype=torch.int32, device="cuda")
+    y = torch.full((40, 64), 7.0, dtype=BF16, device="cuda")
+    lq.lq_conv_prefill(x, w, y=y, cu=cu)
+    assert (y[:5] == 7).all() and (y[30:] == 7).all()
+    ry, _, mag = R.conv(x, w, None, "silu", None, cu)
+    _close(y[5:30], ry[5:30], _conv_tol(ry, mag, BF16, 4, "silu")[5:30], "conv inner rows")
+
+
+# -- selective scan ---------------------------------------------------------------
+
+def _ssm_inputs(seed, lead, B, H, G, dk, dv, dtype, pad=8):
+    g = _gen(seed)
+    wide = _randn(g, (*lead, pad + H * dv + 2 * G * dk), scale=0.7).to(dtype)
+    x = wide[..., pad:pad + H * dv].unflatten(-1, (H, dv))
+    Bm = wide[..., pad + H * dv:pad + H * dv + G * dk].unflatten(-1, (G, dk))
+    Cm = wide[..., pad + H * dv + G * dk:].unflatten(-1, (G, dk))
+    dt = _randn(g, (*lead, H), dtype)
+    A = -(1 + 15 * torch.rand((H,), generator=g, device="cuda"))
+    step = torch.exp(torch.rand((H,), generator=g, device="cuda") * math.log(100) + math.log(1e-3))
+    return {"x": x, "dt": dt, "A": A, "Bm": Bm, "Cm": Cm, "D": 1 + _randn(g, (H,), scale=0.1),
+            "dt_bias": step + torch.log(-torch.expm1(-step)), "S0": _randn(g, (B, H, dk, dv), scale=0.3)}
+
+
+def _ssm_tol(y, S, my, mS, n, dtype, dk):
+    k = (24 * math.sqrt(max(n, 1)) + 8 * math.sqrt(dk) + 64) * R.U
+    return R.half_step(dtype) * (1 + 1e-3) * y.abs() + k * my + R.tiny(dtype), k * mS + 1e-30
+
+
+def _check_ssm(v, cu, what, softplus=True, **kw):
+    a = {**v, **kw}
+    dtype, dk = v["x"].dtype, v["Bm"].shape[-1]
+    y, S = lq.lq_ssm_prefill(a["x"], a["dt"], a["A"], a["Bm"], a["Cm"], D=a["D"], dt_bias=a["dt_bias"],
+                             softplus=softplus, S0=a["S0"], cu=cu)
+    ry, rS, my, mS, n = R.ssm(a["x"], a["dt"], a["A"], a["Bm"], a["Cm"], a["D"], a["dt_bias"], softplus, a["S0"], cu)
+    ty, tS = _ssm_tol(ry, rS, my, mS, n, dtype, dk)
+    _close(y, ry, ty, f"{what} y")
+    _close(S, rS, tS, f"{what} S")
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("H,G,dk,dv", [(2, 1, 64, 64), (3, 3, 128, 64), (4, 2, 64, 128), (5, 1, 128, 128), (6, 2, 128, 64)])
+def test_ssm_packed(dtype, H, G, dk, dv):
+    """Sequences of no token, one token and lengths around the chunks' ends."""
+    _gpu()
+    lens = [0, 1, 2, 15, 16, 17, 63, 64, 65, 0, 127, 128, 129, 200]
+    cu = _cu(lens)
+    v = _ssm_inputs(H * dk + dv, (int(cu[-1]),), len(lens), H, G, dk, dv, dtype)
+    _check_ssm(v, cu, f"ssm {ids(dtype)} H{H} G{G} {dk}x{dv}")
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("T", [0, 1, 3, 100, 130])
+def test_ssm_time_major(dtype, T):
+    _gpu()
+    v = _ssm_inputs(T, (T, 3), 3, 4, 2, 64, 64, dtype)
+    _check_ssm(v, None, f"ssm time-major {ids(dtype)} T{T}")
+    _check_ssm(v, None, f"ssm bare {ids(dtype)} T{T}", D=None, dt_bias=None, S0=None)
+
+
+def test_ssm_rows_not_16_byte_aligned():
+    _gpu()
+    for dtype in TYPES:
+        v = _ssm_inputs(3, (300,), 1, 2, 1, 128, 64, dtype, pad=1)
+        assert v["x"].data_ptr() % 16 != 0
+        _check_ssm(v, _cu([300]), f"ssm odd base {ids(dtype)}")
+
+
+def test_ssm_without_softplus():
+    """d_t used as given: zero steps leave the state, negative log decays as usual."""
+    _gpu()
+    for dtype in TYPES:
+        v = _ssm_inputs(4, (140,), 2, 2, 1, 64, 128, dtype)
+        v["dt"] = (v["dt"].abs() * 0.05).to(dtype)
+        v["dt"][3:9] = 0
+        v["dt_bias"] = None
+        _check_ssm(v, _cu([100, 40]), f"ssm no softplus {ids(dtype)}", softplus=False)
+
+
+def test_ssm_long_sequence():
+    """One sequence of 3001 tokens beside short ones: split along the sequence."""
+    _gpu()
+    for dtype in TYPES:
+        cu = _cu([5, 3001, 0, 40])
+        v = _ssm_inputs(6, (int(cu[-1]),), 4, 2, 1, 64, 64, dtype)
+        _check_ssm(v, cu, f"ssm long {ids(dtype)}")
+
+
+def test_ssm_extreme_steps():
+    """Steps of 0, of 1e-30 and so large that a token wipes the state: no
+    inf - inf inside a chunk, and what follows depends on the wiping token on."""
+    _gpu()
+    for dtype in (F32, BF16):
+        v = _ssm_inputs(7, (200,), 1, 2, 1, 128, 64, dtype)
+        v["dt"] = (v["dt"].abs() * 0.02).to(dtype)
+        v["dt"][10] = 0.0
+        v["dt"][20] = 1e-30
+        v["dt"][50] = 100.0
+        v["dt"][127] = 100.0
+        v["dt"][128] = 100.0
+        v["dt_bias"] = None
+        _check_ssm(v, _cu([200]), f"ssm extreme {ids(dtype)}", softplus=False)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+def test_ssm_non_finite_inputs_reach_only_what_follows(dtype):
+    """An inf or NaN in one token's x, B, C or step leaves every earlier output
+    and the other sequences as they are, and shows in what it touches."""
+    _gpu()
+    for name in ("x", "Bm", "Cm", "dt"):
+        for bad in (float("inf"), float("nan")):
+            lens = [90, 150, 20]
+            cu = _cu(lens)
+            v = _ssm_inputs(8, (260,), 3, 2, 1, 64, 64, dtype)
+            args = lambda u: (u["x"], u["dt"], u["A"], u["Bm"], u["Cm"])   # noqa: E731
+            y0, S0 = lq.lq_ssm_prefill(*args(v), D=v["D"], dt_bias=v["dt_bias"], cu=cu)
+            t = 90 + 70
+            u = {k: (w.clone() if k == name else w) for k, w in v.items()}
+            if name == "dt":
+                u[name][t, 1] = bad
+            else:
+                u[name][t, 0, 5] = bad
+            y1, S1 = lq.lq_ssm_prefill(*args(u), D=v["D"], dt_bias=v["dt_bias"], cu=cu)
+            assert torch.equal(y1[:t], y0[:t]) and torch.equal(y1[240:], y0[240:]), (name, bad)
+            assert torch.equal(S1[0], S0[0]) and torch.equal(S1[2], S0[2])
+            h = 1 if name == "dt" else 0
+            assert not torch.isfinite(y1[t, h]).all(), (name, bad)
+            if name == "Cm":
+                assert torch.equal(S1, S0) and torch.equal(y1[t + 1:], y0[t + 1:])
+            else:
+                assert not torch.isfinite(S1[1, h]).all()
+            if name == "x":       # one value column of one head
+                ok = [c for c in range(64) if c != 5]
+                assert torch.equal(y1[:, 1], y0[:, 1]) and torch.equal(y1[:, 0, ok], y0[:, 0, ok])
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("B,H,G,dk,dv", [(1, 16, 1, 128, 64), (2, 3, 3, 64, 64), (40, 8, 2, 128, 128), (300, 2, 1, 64, 128)])
+def test_ssm_step(dtype, B, H, G, dk, dv):
+    _gpu()
+    v = _ssm_inputs(B + dk, (B,), B, H, G, dk, dv, dtype, pad=3)
+    S = v["S0"].clone()
+    y = lq.lq_ssm_step(S, v["x"], v["dt"], v["A"], v["Bm"], v["Cm"], D=v["D"], dt_bias=v["dt_bias"])
+    one = lambda t: t[None]   # noqa: E731
+    ry, rS, my, mS, n = R.ssm(one(v["x"]), one(v["dt"]), v["A"], one(v["Bm"]), one(v["Cm"]), v["D"], v["dt_bias"], True,
+                              v["S0"], None)
+    ty, tS = _ssm_tol(ry[0], rS, my[0], mS, 1, dtype, dk)
+    _close(y, ry[0], ty, f"ssm step {ids(dtype)} y")
+    _close(S, rS, tS, f"ssm step {ids(dtype)} S")
+
+
+def test_ssm_prompt_in_parts_and_steps():
+    """A prompt in two calls with the state in place, then single tokens."""
+    _gpu()
+    v = _ssm_inputs(9, (260, 2), 2, 4, 1, 128, 64, F32)
+    S = v["S0"].clone()
+    kw = {"D": v["D"], "dt_bias": v["dt_bias"]}
+    ys = []
+    for a, b in ((0, 150), (150, 250)):
+        y, _ = lq.lq_ssm_prefill(*(v[k][a:b] if k != "A" else v[k] for k in ("x", "dt", "A", "Bm", "Cm")), S0=S, S_out=S, **kw)
+        ys.append(y)
+    for t in range(250, 260):
+        ys.append(lq.lq_ssm_step(S, *(v[k][t] if k != "A" else v[k] for k in ("x", "dt", "A", "Bm", "Cm")), **kw)[None])
+    ry, rS, my, mS, n = R.ssm(v["x"], v["dt"], v["A"], v["Bm"], v["Cm"], v["D"], v["dt_bias"], True, v["S0"], None)
+    ty, tS = _ssm_tol(ry, rS, my, mS, n, F32, 128)
+    _close(torch.cat(ys), ry, ty, "ssm parts y")
+    _close(S, rS, tS, "ssm parts S")
+
+
+def test_ssm_rows_outside_the_sequences_stay():
+    _gpu()
+    for dtype in TYPES:
+        v = _ssm_inputs(2, (300,), 2, 2, 1, 64, 64, dtype)
+        cu = torch.tensor([7, 60, 280], dtype=torch.int32, device="cuda")
+        y = torch.full((300, 2, 64), 7.0, dtype=dtype, device="cuda")
+        lq.lq_ssm_prefill(v["x"], v["dt"], v["A"], v["Bm"], v["Cm"], y=y, cu=cu)
+        assert (y[:7] == 7).all() and (y[280:] == 7).all() and not (y[7:280] == 7).all(-1).any()
+
+
+# -- norms --------------------------------------------------------------------------
+
+def _norm_tol(y, terms, dtype, D, act):
+    # statistic: D squares summed (probabilistic), its root halves the error
+    k = (4 * math.sqrt(D) + 12) * R.U + _act_rel(dtype, act)
+    return R.half_step(dtype) * (1 + 1e-3) * y.abs() + 2 * k * terms + R.tiny(dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("rows,D", [(1, 1), (3, 7), (5, 64), (9, 129), (4, 512), (2, 1000), (3, 2048), (2, 4096), (2, 4097),
+                                    (2, 8192), (1, 16384), (1, 16383)])
+def test_norm_in(dtype, rows, D):
+    _gpu()
+    g = _gen(D)
+    x, res = _randn(g, (rows, D), dtype), _randn(g, (rows, D), dtype, 3.0)
+    w, vec = 1 + _randn(g, (D,), scale=0.2), torch.rand((D,), generator=g, device="cuda")
+    for r, sc in ((res, vec), (res, 0.25), (None, 1.0)):
+        y, h = lq.lq_norm_in(x, w, res=r, scale=sc, eps=1e-5)
+        s64 = sc.double() if isinstance(sc, torch.Tensor) else sc
+        ry, rh = R.norm_in(x, w, r, s64, 1e-5)
+        terms = ((s64 * x.double()).abs() + (0 if r is None else r.double().abs()))
+        inv = 1 / torch.sqrt((rh * rh).mean(-1, keepdim=True) + 1e-5)
+        _close(h, rh, R.half_step(dtype) * (1 + 1e-3) * rh.abs() + 2 * R.U * terms + R.tiny(dtype), f"h {ids(dtype)} {D}")
+        _close(y, ry, _norm_tol(ry, ry.abs() + terms * inv * w.double().abs(), dtype, D, None), f"norm_in {ids(dtype)} {D}")
+
+
+@pytest.mark.parametrize("dtype,xt", [(F32, F32), (BF16, BF16), (F16, F16), (BF16, F32), (F16, F32)], ids=ids)
+@pytest.mark.parametrize("rows,G,D", [(1, 1, 1), (5, 3, 47), (7, 16, 128), (3, 2, 64), (33, 1, 2048), (2, 2, 4104), (1, 1, 16384)])
+def test_norm_out(dtype, xt, rows, G, D):
+    _gpu()
+    g = _gen(D + rows)
+    x = _randn(g, (rows, G, D), xt, 0.5)
+    z = _randn(g, (rows, G * D + 16), dtype, 2.0)[:, 16:].unflatten(-1, (G, D))    # columns of a projection
+    res = _randn(g, (rows, G, D), dtype, 3.0)
+    w1, w2 = 1 + _randn(g, (D,), scale=0.2), 1 + _randn(g, (G, D), scale=0.2)
+    vec = torch.rand((G, D), generator=g, device="cuda")
+    for w, zz, act, first, r, sc in ((w1, z, "silu", False, None, 1.0), (w2, z, "sigmoid", True, res, vec),
+                                     (w2, z, "silu", True, res, 0.5), (w1, None, "silu", False, None, 2.0)):
+        y = lq.lq_norm_out(x, w, z=zz, act=act, gate_first=first, res=r, scale=sc, eps=1e-6, y=torch.empty_like(res))
+        s64 = sc.double() if isinstance(sc, torch.Tensor) else sc
+        ry = R.norm_out(x, w, zz, act, first, r, s64, 1e-6)
+        inner = R.norm_out(x, w, zz, act, first, None, s64, 1e-6).abs()
+        _close(y, ry, _norm_tol(ry, inner + ry.abs(), dtype, D, act if zz is not None else None),
+               f"norm_out {ids(dtype)} {G}x{D} {act} first={first}")
+
+
+def test_norms_in_place_and_zero_rows():
+    _gpu()
+    g = _gen(3)
+    x, res, w = _randn(g, (6, 256), BF16), _randn(g, (6, 256), BF16), _randn(g, (256,))
+    y0, h0 = lq.lq_norm_in(x, w, res=res, scale=0.5)
+    a, b = x.clone(), res.clone()
+    y1, h1 = lq.lq_norm_in(a, w, res=b, scale=0.5, y=a, h=b)
+    assert torch.equal(y0, y1) and torch.equal(h0, h1) and y1 is a and h1 is b
+    x3, z3, r3 = (t.view(6, 2, 128) for t in (x, res, h0))
+    want = lq.lq_norm_out(x3, w[:128], z=z3, res=r3)
+    for alias in range(3):
+        t = [v.clone() for v in (x3, z3, r3)]
+        got = lq.lq_norm_out(t[0], w[:128], z=t[1], res=t[2], y=t[alias])
+        assert torch.equal(got, want), alias
+    assert (lq.lq_norm_in(torch.zeros_like(x), w)[0] == 0).all()
+    assert lq.lq_norm_in(x[:0], w)[0].shape == (0, 256)
+    # all-zero rows and a row with an infinity stay apart
+    x[2] = 0
+    x[3, 5] = float("inf")
+    y, _ = lq.lq_norm_in(x, w)
+    assert (y[2] == 0).all() and torch.isfinite(y[[0, 1, 2, 4, 5]]).all() and not torch.isfinite(y[3]).all()
+
+
+# -- streams, graphs, chains ----------------------------------------------------------
+
+def test_side_stream_and_graph_replay():
+    """Calls on a stream of the caller's, and captured and replayed, give the
+    eager call's bits."""
+    _gpu()
+    v = _ssm_inputs(11, (600,), 3, 4, 1, 128, 64, BF16)
+    cu = _cu([400, 1, 199])
+    g = _gen(12)
+    w, wn = _randn(g, (256, 4)), _randn(g, (64,))
+    xc = v["x"].reshape(600, 256)
+
+    def chain(stream=None):
+        xs, _ = lq.lq_conv_prefill(xc, w, cu=cu, stream=stream)
+        y, S = lq.lq_ssm_prefill(xs.view(600, 4, 64), v["dt"], v["A"], v["Bm"], v["Cm"], D=v["D"],
+                                 dt_bias=v["dt_bias"], S0=v["S0"], cu=cu, stream=stream)
+        return lq.lq_norm_out(y, wn, z=v["x"], res=y, scale=0.5, stream=stream), S
+    want = chain()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = chain(s)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = chain()
+    for _ in range(2):
+        for t in out:
+            t.fill_(float("nan"))
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(want, out))
+
+
+def test_same_inputs_same_bits():
+    _gpu()
+    for dtype in TYPES:
+        v = _ssm_inputs(13, (1500,), 2, 4, 2, 64, 64, dtype)
+        cu = _cu([1300, 200])
+        a = [lq.lq_ssm_prefill(v["x"], v["dt"], v["A"], v["Bm"], v["Cm"], S0=v["S0"], cu=cu) for _ in range(3)]
+        assert all(torch.equal(a[0][i], b[i]) for b in a[1:] for i in range(2))
