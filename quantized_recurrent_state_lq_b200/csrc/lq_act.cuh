@@ -173,7 +173,7 @@ __device__ __forceinline__ bool find_piece(const Rows &r, int seg, int id, Piece
     return p.j >= 0 && p.j < p.n;
 }
 
-inline int64_t piece_count(const Rows &r, int seg) {
+__host__ __device__ inline int64_t piece_count(const Rows &r, int seg) {
     if (r.cu) return (int64_t)(r.rows / seg) + r.B;
     const int T = r.rows / r.B;
     return (int64_t)r.B * (T > 0 ? ((int64_t)T + seg - 1) / seg : 1);

@@ -10,7 +10,7 @@
 // the GPU (16 16-byte loads in flight per thread), 16 when they do not (four
 // times the CTAs, a quarter of the serial work each).  The state stays in
 // registers over the tokens of a short prompt.
-#include "lq_act.cuh"
+#include "lq_ssm.h"
 
 namespace lq {
 namespace {
@@ -119,8 +119,81 @@ cudaError_t launch_ssm_step(const SsmArgs &a, int dtype, cudaStream_t s) {
     return step_sizes<f16>(a, s);
 }
 
-size_t ssm_ws_bytes(int, int, int, int, int, int, int) { return 0; }
+namespace {
 
-cudaError_t launch_ssm_prefill(const SsmArgs &a, int dtype, cudaStream_t s) { return launch_ssm_step(a, dtype, s); }
+// One thread per 4 state elements of one sequence and head.
+__global__ void __launch_bounds__(256) ssm_join_kernel(SsmArgs a, int seg) {
+    const int64_t per = (int64_t)a.dk * a.dv / 4;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;   // (head, element), same sequence for the CTA row
+    if (i >= per * a.H) return;
+    for (int b = blockIdx.y; b < a.r.B; b += gridDim.y) {
+        int64_t z0;
+        int n;
+        if (a.r.cu) {
+            const int c0 = cu_at(a.r, b), len = max(cu_at(a.r, b + 1), c0) - c0;
+            z0 = c0 / seg + b;
+            n = (len + seg - 1) / seg;
+        } else {
+            n = (a.r.rows / a.r.B + seg - 1) / seg;
+            z0 = (int64_t)b * n;
+        }
+        if (n < 2) continue;
+        const int h = (int)(i / per);
+        const float *decay = ssm_decays(a, seg) + z0 * a.H + h;
+        float4 *slot = reinterpret_cast<float4 *>(a.ws) + z0 * a.H * per + i;
+        float4 S = a.S0 ? reinterpret_cast<const float4 *>(a.S0)[(int64_t)b * a.H * per + i]
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 own = slot[0];
+        for (int j = 0; j < n; ++j) {
+            float4 *at = slot + (int64_t)j * a.H * per;
+            float4 next = own;
+            if (j + 2 < n) next = at[a.H * per];   // the last piece has no state of its own
+            *at = S;
+            if (j + 1 < n) {
+                const float k = decay[(int64_t)j * a.H];
+                S = make_float4(fmaf(k, S.x, own.x), fmaf(k, S.y, own.y), fmaf(k, S.z, own.z), fmaf(k, S.w, own.w));
+            }
+            own = next;
+        }
+    }
+}
+
+// Tokens per piece.  One CTA takes one piece of 64 value columns of a head and
+// two run on each SM: pieces are cut so that the batch gives about that many.
+// A batch with enough sequences and heads is cut only where a sequence is
+// longer than a CTA's share of all tokens.
+int piece_tokens(const Rows &r, int H, int dv) {
+    const int64_t units = (int64_t)H * dv / 64, slots = 148 * 2;
+    const int64_t share = units <= slots ? (r.rows + slots / units - 1) / (slots / units)
+                                         : (r.rows * units + slots - 1) / slots;
+    const int64_t seg = (share + 127) / 128 * 128;
+    return (int)(seg < 128 ? 128 : seg > (1 << 30) ? (1 << 30) : seg);
+}
+
+// Whether a sequence can be longer than a piece.
+bool may_split(const Rows &r, int seg) { return (r.cu ? r.rows : r.rows / r.B) > seg; }
+
+}  // namespace
+
+cudaError_t launch_ssm_join(const SsmArgs &a, int seg, cudaStream_t s) {
+    const int64_t n = (int64_t)a.H * a.dk * a.dv / 4;
+    ssm_join_kernel<<<dim3((unsigned)((n + 255) / 256), a.r.B < 65535 ? a.r.B : 65535), 256, 0, s>>>(a, seg);
+    return cudaGetLastError();
+}
+
+size_t ssm_ws_bytes(int dtype, int B, int rows, int H, int G, int dk, int dv) {
+    if (dtype != kBF16) return 0;
+    Rows r{nullptr, B, rows};
+    const int seg = piece_tokens(r, H, dv);
+    if (rows <= seg) return 0;
+    // packed: at most rows / seg + B pieces, no fewer than time-major ones
+    return ((size_t)(rows / seg + B) * H * (dk * dv + 1) * 4 + 255) / 256 * 256;
+}
+
+cudaError_t launch_ssm_prefill(const SsmArgs &a, int dtype, cudaStream_t s) {
+    if (dtype != kBF16 || a.r.rows <= 0) return launch_ssm_step(a, dtype, s);
+    const int seg = piece_tokens(a.r, a.H, a.dv);
+    return launch_ssm_umma(a, seg, may_split(a.r, seg), s);
+}
 
 }  // namespace lq
