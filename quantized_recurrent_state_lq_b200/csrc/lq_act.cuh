@@ -143,11 +143,13 @@ struct Piece {
     int len;      // the sequence's tokens
     int n;        // pieces of the sequence
     int64_t row0, step;   // row of token t: row0 + t * step
+    int64_t id;           // its number
 };
 
 __device__ __forceinline__ int cu_at(const Rows &r, int i) { return min(max(r.cu[i], 0), r.rows); }
 
 __device__ __forceinline__ bool find_piece(const Rows &r, int seg, int id, Piece &p) {
+    p.id = id;
     if (!r.cu) {
         p.len = r.rows / r.B;
         p.n = max(1, (p.len + seg - 1) / seg);
@@ -173,10 +175,35 @@ __device__ __forceinline__ bool find_piece(const Rows &r, int seg, int id, Piece
     return p.j >= 0 && p.j < p.n;
 }
 
+// The k-th place where a sequence may be cut: piece j of a sequence whose piece
+// j + 1 exists.  Sequence b's are floor(cu[b] / seg) + j, j < n - 1, disjoint as
+// above, below rows / seg.
+__device__ __forceinline__ bool find_cut(const Rows &r, int seg, int k, Piece &p) {
+    if (!r.cu) {
+        const int cuts = (r.rows / r.B - 1) / seg;
+        const int b = k / cuts;
+        return b < r.B && find_piece(r, seg, b * (cuts + 1) + k % cuts, p);
+    }
+    int lo = 0, hi = r.B - 1;   // the last b whose first number is <= k
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cu_at(r, mid) / seg <= k) lo = mid;
+        else hi = mid - 1;
+    }
+    const int first = cu_at(r, lo) / seg;
+    return k >= first && find_piece(r, seg, k + lo, p) && p.b == lo && p.j < p.n - 1;
+}
+
 __host__ __device__ inline int64_t piece_count(const Rows &r, int seg) {
     if (r.cu) return (int64_t)(r.rows / seg) + r.B;
     const int T = r.rows / r.B;
     return (int64_t)r.B * (T > 0 ? ((int64_t)T + seg - 1) / seg : 1);
+}
+
+inline int64_t cut_count(const Rows &r, int seg) {
+    if (r.cu) return r.rows / seg;
+    const int T = r.rows / r.B;
+    return T > seg ? (int64_t)r.B * ((T - 1) / seg) : 0;
 }
 
 }  // namespace lq

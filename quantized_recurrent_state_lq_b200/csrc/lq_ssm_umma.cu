@@ -12,23 +12,30 @@
 // registers.  Every decay factor is 2^(difference), later token first, so a
 // decaying state never forms a factor above 1.
 //
-// A CTA of four warps takes 64 value columns of one head over one piece of a
-// sequence; thread r is token r, key row r and tensor-memory lane r.  Phases
-// alternate between the tensor core and the threads, and two CTAs per SM (256
-// tensor-memory columns, 112 KB of shared memory each) fill each other's gaps.
+// A group of eight warps takes 64 value columns of one head over one piece of
+// a sequence: two threads per token, key row and tensor-memory lane, 32 columns
+// each, and a ninth warp that issues the group's copies and MMAs.  Its phases
+// alternate between the tensor core and the threads, so a CTA runs two groups
+// (256 tensor-memory columns, 112 KB of shared memory each) half a chunk apart:
+// a kernel that uses tensor memory gets one CTA per SM here.
 // Long sequences of a small batch are cut into pieces: a first pass forms each
 // piece's own state, ssm_join_kernel chains them, the second pass starts every
 // piece from its state (about a third more work for pieces x as much
 // parallelism).
 //
-// Shared memory holds every operand as 16-byte chunks of 8 columns, chunk
-// column j of 128 rows at 2048 j, row t at 16 t: read as rows x K it is
-// K-major without swizzle, read as K x columns it is MN-major, so B serves
-// C B^T and B^T X' from one copy.  A warp's 16-byte accesses touch 8
-// consecutive rows of a chunk column (no bank conflicts).
+// Shared memory holds every operand as rows of 64 columns (128 bytes, the
+// 16-byte chunks XOR-swizzled by the row's low 3 bits) in blocks of 16 KB:
+// read as rows x K it is K-major, read as K x columns MN-major, so B serves
+// C B^T and B^T X' from one copy, and a thread's accesses to its own row meet
+// no bank conflict.  B, C and X arrive by TMA tensor copies, issued as soon as
+// the chunk before has let go of their places:
 //   [0, 32K) C, [32K, 64K) S parts   -- until C B^T and C S are done; then
 //   [0, 48K) X' parts, [48K, ..) decay factors
 //   [64K, 96K) B, [96K, 112K) X
+// Rows that TMA cannot take (not 16-byte aligned) are copied by the threads.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "lq_act.cuh"
 #include "lq_ssm.h"
 #include "lq_tc.cuh"
@@ -37,11 +44,13 @@ namespace lq {
 namespace {
 
 constexpr int Q = 128;                 // tokens per chunk
-constexpr int PW = 64;                 // value columns per CTA
-constexpr int kNT = 128;
-constexpr uint32_t kChunkB = Q * 16;   // bytes of a chunk column
-constexpr int kOffC = 0, kOffS = 32768, kOffXw = 0, kOffF = 49152, kOffB = 65536, kOffX = 98304;
-constexpr int kSmem = 114688;
+constexpr int PW = 64;                 // value columns of a group
+constexpr int HW = PW / 2;             // and of a thread
+constexpr int kNT = 256;               // computing threads of a group
+constexpr int kThreadsAll = 2 * kNT + 64;
+constexpr int kBlk = Q * 128;          // bytes of 128 rows of 64 columns
+constexpr int kOffC = 0, kOffS = 2 * kBlk, kOffXw = 0, kOffF = 3 * kBlk, kOffB = 4 * kBlk, kOffX = 6 * kBlk;
+constexpr int kSmem = 7 * kBlk;
 constexpr uint32_t kTmemCols = 256, kColY = 128, kColS = 192;   // G and M: columns 0..127
 
 // Instruction descriptors, kind::f16 with bf16 operands and FP32 accumulators.
@@ -68,15 +77,30 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t at, uint64_t bd, uin
         : "memory");
 }
 
-// K-major: 8-row groups 128 B apart, chunk columns along K 2048 B apart.
-__device__ __forceinline__ uint64_t desc_k(const void *p) { return umma_smem_desc(p, kChunkB, 128); }
-// MN-major: 8-row groups along K 128 B apart, chunk columns 2048 B apart.
-__device__ __forceinline__ uint64_t desc_mn(const void *p) { return umma_smem_desc(p, 128, kChunkB); }
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool full) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(full ? 16 : 0) : "memory");
+// 128-byte swizzle: 8-row groups 1024 B apart; MN-major operands of more than
+// 64 columns continue a block further.
+__device__ __forceinline__ uint64_t desc_sw(const void *p, uint32_t lbo) {
+    return umma_smem_desc(p, lbo, 1024) | (2ull << 61);
 }
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ uint64_t desc_k(const void *p) { return desc_sw(p, 16); }
+__device__ __forceinline__ uint64_t desc_mn(const void *p) { return desc_sw(p, kBlk); }
+// 16 further along K: 32 bytes of a K-major block's rows (4 steps a block), 16
+// rows of an MN-major one.
+__device__ __forceinline__ constexpr uint64_t step_k(int k) { return (uint64_t)((k >> 2) * kBlk + (k & 3) * 32) >> 4; }
+__device__ __forceinline__ constexpr uint64_t step_mn(int k) { return (uint64_t)(k * 16 * 128) >> 4; }
+
+// 16-byte chunk j of a row.
+__device__ __forceinline__ uint4 *chunk(unsigned char *tile, int row, int j) {
+    return reinterpret_cast<uint4 *>(tile + (j >> 3) * kBlk + row * 128 + (((j & 7) ^ (row & 7)) << 4));
+}
+
+__device__ __forceinline__ void tma_rows(void *dst, const CUtensorMap *map, int col, int b, int t, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(col), "r"(b), "r"(t), "r"(smem_u32(bar))
+        : "memory");
+}
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -97,315 +121,409 @@ __device__ __forceinline__ uint32_t last_part(float a, float b) {
     return *reinterpret_cast<const uint32_t *>(&p);
 }
 
-// Rows t0 .. t0 + Q - 1 of a sequence (zeros from `len` on), NCH chunks of 8
-// elements each, into chunk columns.
-template <int NCH>
-__device__ __forceinline__ void load_tile(unsigned char *dst, const bf16 *src, int64_t ld, const Piece &p, int t0,
-                                          bool vec) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// Rows t0 .. t0 + Q - 1 of a sequence (zeros from its end on), NCH chunks of 8
+// elements each, element by element: thread i of the group.
+__device__ __forceinline__ void copy_tile(unsigned char *dst, int nch, const bf16 *src, int64_t ld, const Piece &p,
+                                          int t0, int i) {
+    for (; i < Q * nch; i += kNT) {
+        const int t = i / nch, j = i % nch;
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+        if (t0 + t < p.len) {
+            const uint16_t *e = reinterpret_cast<const uint16_t *>(src + (p.row0 + (t0 + t) * p.step) * ld + 8 * j);
 #pragma unroll
-    for (int i = 0; i < 16 * (NCH / 4) / 4; ++i) {
-        const int grp = i * 4 + warp;                 // 8 rows x 4 chunks
-        const int t = (grp & 15) * 8 + (lane & 7), j = (grp >> 4) * 4 + (lane >> 3);
-        const bool in = t0 + t < p.len;
-        const bf16 *s = src + (p.row0 + (in ? t0 + t : t0) * p.step) * ld + 8 * j;
-        unsigned char *d = dst + j * kChunkB + t * 16;
-        if (vec) {
-            cp_async16(smem_u32(d), s, in);
-        } else {
-            uint32_t w[4] = {0u, 0u, 0u, 0u};
-            const uint16_t *e = reinterpret_cast<const uint16_t *>(s);
-            if (in)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) w[k] = (uint32_t)e[2 * k] | ((uint32_t)e[2 * k + 1] << 16);
-            *reinterpret_cast<uint4 *>(d) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int k = 0; k < 4; ++k) w[k] = (uint32_t)e[2 * k] | ((uint32_t)e[2 * k + 1] << 16);
         }
+        *chunk(dst, t, j) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
+// Token rows [T][B][width] of x, B and C as 3-D maps, boxes of 64 columns x 128
+// tokens of one sequence (packed: one sequence of all rows).
+struct alignas(64) SsmMaps {
+    CUtensorMap x, b, c;
+};
+
 struct Fixed {
-    uint64_t bar[3];     // G and C S done, Y done, B^T X' done
+    uint64_t bar[4];     // G and C S done, Y done, B^T X' done, tiles arrived
     double wsum[4];      // each warp's log2 decay
-    uint32_t tmem;
     int bad;             // a wait ran out
-    int nf;              // a non-finite x in this chunk
-    int first[PW];       // per value column, the first token whose x is not finite
+    int nf[2];           // a non-finite x in this chunk (even, odd chunks)
+    int first[2][PW];    // per value column, the first token whose x is not finite
 };
 
 // FULL: outputs and the final state; else only the pieces' own states (from
 // zero) and decays, for all but the last piece of each sequence.
 template <bool FULL, int DK>
-__global__ void __launch_bounds__(kNT, 2) ssm_umma_kernel(SsmArgs a, int seg, int units, int vec, int split) {
-    extern __shared__ __align__(128) unsigned char sm[];
-    __shared__ Fixed fx;
-    const int r = threadIdx.x, warp = r >> 5, lane = r & 31;
-    const int z = blockIdx.x / units, u = blockIdx.x % units;
+__global__ void __launch_bounds__(kThreadsAll, 1)
+    ssm_umma_kernel(SsmArgs a, const __grid_constant__ SsmMaps maps, int seg, int units, int tma, int split) {
+    extern __shared__ __align__(1024) unsigned char smem[];
+    __shared__ uint32_t tmem;
+    const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool issuer = wid >= 2 * kNT / 32;
+    const int grp = issuer ? wid - 2 * kNT / 32 : threadIdx.x / kNT;
+    unsigned char *sm = smem + grp * kSmem;
+    Fixed &fx = reinterpret_cast<Fixed *>(smem + 2 * kSmem)[grp];
+    const int warp = wid & 3, half = (wid >> 2) & 1, r = warp * 32 + lane;   // 32 rows, 32 columns of this warp
+    const int pairs = (units + 1) / 2;
+    const int z = blockIdx.x / pairs, u = 2 * (blockIdx.x % pairs) + grp;
     Piece p;
-    if (!find_piece(a.r, seg, z, p) || (!FULL && p.j >= p.n - 1)) return;
+    if (!(FULL ? find_piece(a.r, seg, z, p) : find_cut(a.r, seg, z, p))) return;
+    const bool idle = u >= units;   // the second group of an odd number of units
+    // barriers of the group: with its issuing warp, and without
+    auto sync_all = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(kNT + 32) : "memory"); };
+    auto sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(3 + grp), "n"(kNT) : "memory"); };
     const int per = a.dv / PW;
-    const int h = u / per, c0 = (u % per) * PW;
+    const int h = idle ? 0 : u / per, c0 = (u % per) * PW;
     const int g = (int)((int64_t)h * a.G / a.H);
-    const bf16 *xp = static_cast<const bf16 *>(a.x) + (int64_t)h * a.dv + c0;
-    const bf16 *bp = static_cast<const bf16 *>(a.Bm) + g * DK;
-    const bf16 *cp = static_cast<const bf16 *>(a.Cm) + g * DK;
-    const bf16 *dp = static_cast<const bf16 *>(a.dt) + h;
-    const float A2 = a.A[h] * 1.4426950408889634f;   // log2 decay per unit step
-    const float Dh = a.D ? a.D[h] : 0.0f, bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
+    const int t_first = p.j * seg, t_end = idle ? t_first : min(p.len, t_first + seg);
 
-    if (warp == 0) tmem_alloc(&fx.tmem, kTmemCols);
-    if (r == 0) {
-        for (int i = 0; i < 3; ++i) mbar_init(&fx.bar[i], 1);
+    if (wid == 0) tmem_alloc(&tmem, 2 * kTmemCols);
+    if (issuer && lane == 0) {
+        for (int i = 0; i < 4; ++i) mbar_init(&fx.bar[i], 1);
         fx.bad = 0;
         fence_mbar_init();
     }
-    if (DK < 128) {   // B^T has 128 rows: the missing key rows are zero
-        for (int i = r; i < (128 - DK) / 8 * (int)kChunkB / 16; i += kNT)
-            reinterpret_cast<uint4 *>(sm + kOffB + DK / 8 * kChunkB)[i] = make_uint4(0u, 0u, 0u, 0u);
-    }
-
-    // The state's key row r, this CTA's columns.
-    float S[PW];
-    const int64_t soff = ((int64_t)h * DK + r) * a.dv + c0, sall = (int64_t)a.H * DK * a.dv;
-    const float *S0 = nullptr;
-    if (FULL && r < DK) {
-        if (split && p.n > 1) S0 = a.ws + z * sall + soff;
-        else if (a.S0) S0 = a.S0 + p.b * sall + soff;
-    }
-#pragma unroll
-    for (int i = 0; i < PW / 4; ++i) {
-        const float4 v = S0 ? reinterpret_cast<const float4 *>(S0)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
-        S[4 * i] = v.x; S[4 * i + 1] = v.y; S[4 * i + 2] = v.z; S[4 * i + 3] = v.w;
-    }
-    double gsum = 0.0;   // log2 decay of the piece so far
-    const int t_end = min(p.len, (p.j + 1) * seg);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = tmem + grp * kTmemCols, tl = tm + ((uint32_t)warp << 21);   // this warp's lanes: 32 warp
     int parity = 0;
-    for (int t0 = p.j * seg; t0 < t_end; t0 += Q, parity ^= 1) {
-        tc_fence_before();
-        __syncthreads();   // the chunk before is done with shared and tensor memory
-        if (fx.bad) break;
-        load_tile<DK / 8>(sm + kOffB, bp, a.ldb, p, t0, vec);
-        load_tile<PW / 8>(sm + kOffX, xp, a.ldx, p, t0, vec);
-        if (FULL) load_tile<DK / 8>(sm + kOffC, cp, a.ldc, p, t0, vec);
-        // This token's step and log2 decay, floored at -150 (a factor FP32
-        // flushes to 0) so that no difference of sums is inf - inf; a NaN
-        // passes the comparison by.
-        float d = 0.0f, l = 0.0f;
-        if (t0 + r < p.len) {
-            d = __bfloat162float(dp[(p.row0 + (t0 + r) * p.step) * a.lddt]) + bias;
-            if (a.softplus) d = softplus_f(d);
-            l = d * A2;
-            if (l < -150.0f) l = -150.0f;
-        }
-        double gw = l;   // inclusive sum within the warp
+
+    if (issuer) {
+        // where TMA finds token t: (row of its sequence, sequence)
+        const int tm_t = a.r.cu ? (int)p.row0 : 0, tm_b = a.r.cu ? 0 : p.b;
+        // B and C of a chunk (their places are free once B^T X' of the chunk
+        // before is done), then X (free once its outputs are written).
+        auto load_bc = [&](int t0) {
+            mbar_arrive_expect_tx(&fx.bar[3], (FULL ? 2 : 1) * (DK / 64) * kBlk + kBlk);
 #pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-            const double o = __shfl_up_sync(0xffffffffu, gw, m);
-            if (lane >= m) gw += o;
-        }
-        if (lane == 31) fx.wsum[warp] = gw;
-        if (r == 0) fx.nf = 0;
-        if (r < PW) fx.first[r] = Q;
-        if (FULL && r < DK) {   // the state's two parts, chunk column by chunk column
-#pragma unroll
-            for (int j = 0; j < PW / 8; ++j) {
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float v0 = S[8 * j + 2 * k], v1 = S[8 * j + 2 * k + 1];
-                    hi[k] = take_part(v0, v1);
-                    lo[k] = last_part(v0, v1);
-                }
-                unsigned char *s = sm + kOffS + j * kChunkB + r * 16;
-                *reinterpret_cast<uint4 *>(s) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4 *>(s + 16384) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            for (int j = 0; j < DK / 64; ++j) {
+                tma_rows(sm + kOffB + j * kBlk, &maps.b, g * DK + 64 * j, tm_b, tm_t + t0, &fx.bar[3]);
+                if (FULL) tma_rows(sm + kOffC + j * kBlk, &maps.c, g * DK + 64 * j, tm_b, tm_t + t0, &fx.bar[3]);
             }
+        };
+        auto load_x = [&](int t0) { tma_rows(sm + kOffX, &maps.x, h * a.dv + c0, tm_b, tm_t + t0, &fx.bar[3]); };
+        if (tma && lane == 0 && t_first < t_end) {
+            load_bc(t_first);
+            load_x(t_first);
         }
-        cp_async_wait();
-        fence_async_smem();
-        __syncthreads();
-        const uint32_t tm = fx.tmem, tl = tm + ((uint32_t)warp << 21);   // this warp's lanes: 32 warp
-        if (FULL && r == 0) {
-            tc_fence_after();
-            const uint64_t cd = desc_k(sm + kOffC), bd = desc_k(sm + kOffB), sd = desc_mn(sm + kOffS);
+        for (int t0 = t_first; t0 < t_end; t0 += Q, parity ^= 1) {
+            sync_all();   // the chunk before is done with shared and tensor memory
+            if (lane == 0 && tma && t0 != t_first) load_x(t0);
+            if (fx.bad) {
+                if (lane == 0 && tma) mbar_wait_bounded(&fx.bar[3], parity, nullptr);   // the copies under way
+                break;
+            }
+            if (!tma || t0 + Q > p.len) sync_all();   // tiles copied or their ends cleared by the threads
+            if (FULL && lane == 0) {
+                if (tma && !mbar_wait_bounded(&fx.bar[3], parity, nullptr)) fx.bad = 1;
+                tc_fence_after();
+                const uint64_t cd = desc_k(sm + kOffC), bd = desc_k(sm + kOffB), sd = desc_mn(sm + kOffS);
 #pragma unroll
-            for (int k = 0; k < DK / 16; ++k)
-                mma_ss(tm, cd + (k * 2 * kChunkB >> 4), bd + (k * 2 * kChunkB >> 4), idesc(Q, 0, 0), k > 0);
-#pragma unroll
-            for (int part = 0; part < 2; ++part)
+                for (int k = 0; k < DK / 16; ++k) mma_ss(tm, cd + step_k(k), bd + step_k(k), idesc(Q, 0, 0), k > 0);
+                // C S, its parts side by side: [kColY, kColS) and [kColS, 256)
 #pragma unroll
                 for (int k = 0; k < DK / 16; ++k)
-                    mma_ss(tm + kColY, cd + (k * 2 * kChunkB >> 4), sd + ((part * 16384 + k * 256) >> 4),
-                           idesc(PW, 0, 1), part + k > 0);
-            umma_commit(&fx.bar[0]);
-        }
-        double base = 0.0, total = 0.0;   // before this warp, and of the chunk
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            if (w < warp) base += fx.wsum[w];
-            total += fx.wsum[w];
-        }
-        const double gt = base + gw;
-        const float wr = d * exp2f((float)(total - gt));   // weight of this token in the next state
-        if (FULL && !mbar_wait_bounded(&fx.bar[0], parity, nullptr)) fx.bad = 1;
-        __syncwarp();
-        tc_fence_after();
-        float *fl = reinterpret_cast<float *>(sm + kOffF);   // [Q] sums within the warp, [Q] d, [3][Q] factors
-        if (FULL) {
-            fl[r] = (float)gw;
-            fl[Q + r] = d;
-            double end = 0.0;   // sum up to warp w: 2^(end - g_s) d_s for the rows of later warps
-#pragma unroll
-            for (int w = 0; w < 3; ++w) {
-                end += fx.wsum[w];
-                if (w >= warp) fl[(2 + w) * Q + r] = d * exp2f((float)(end - gt));
+                    mma_ss(tm + kColY, cd + step_k(k), sd + step_mn(k), idesc(2 * PW, 0, 1), k > 0);
+                umma_commit(&fx.bar[0]);
             }
-        }
-        // X' of this token in three parts; a non-finite x leaves X (times 0 it
-        // would reach earlier tokens) and is marked instead.
+            __syncwarp();
+            sync_all();   // X', M and the scaled C S are in place
+            if (lane == 0) {
+                tc_fence_after();
+                if (FULL) {
+                    const uint64_t xd = desc_mn(sm + kOffX);
 #pragma unroll
-        for (int j = 0; j < PW / 8; ++j) {
-            unsigned char *s = sm + kOffX + j * kChunkB + r * 16;
-            Raw<bf16, 8> rx;
-            rx.a = *reinterpret_cast<const uint4 *>(s);
-            float f[8];
-            rx.get(f);
-            float sum = 0.0f;   // 0 x finite = 0, else NaN
+                    for (int k = 0; k < Q / 16; ++k)
 #pragma unroll
-            for (int k = 0; k < 8; ++k) sum = fmaf(0.0f, f[k], sum);
-            uint32_t w[3][4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                float v0 = wr * f[2 * k], v1 = wr * f[2 * k + 1];
-                w[0][k] = take_part(v0, v1);
-                w[1][k] = take_part(v0, v1);
-                w[2][k] = last_part(v0, v1);
-            }
-#pragma unroll
-            for (int i = 0; i < 3; ++i)
-                *reinterpret_cast<uint4 *>(sm + kOffXw + i * 16384 + j * kChunkB + r * 16) =
-                    make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
-            if (FULL && sum != 0.0f) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (!isfinite(f[k])) {
-                        f[k] = 0.0f;
-                        atomicMin(&fx.first[8 * j + k], r);
-                    }
-                rx.set(f);
-                *reinterpret_cast<uint4 *>(s) = rx.a;
-                fx.nf = 1;
-            }
-        }
-        __syncwarp();
-        if (FULL) {
-            const float et = ex2((float)gt);   // 2^(g_t), on C S
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                uint32_t v[32];
-                tmem_ld_32x32b<32>(tl + kColY + 32 * q, v);
-                tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(et * __uint_as_float(v[i]));
-                tmem_st_32x32b_x32(tl + kColY + 32 * q, v);
-            }
-            __syncthreads();   // the factors
-            // M over G, 32 columns at a time: 16 columns of first parts, 16 of
-            // second.  Columns of earlier warps' tokens factor through the
-            // boundary before this warp, later ones are zero.
-            const float rf = ex2((float)gw);
-            for (int q = 0; q < 4; ++q) {
-                uint32_t v[32];
-                if (q > warp) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = 0u;
-                } else {
-                    tmem_ld_32x32b<32>(tl + 32 * q, v);
-                    tmem_ld_wait();
-                    uint32_t hi[16], lo[16];
-                    if (q < warp) {
-                        const float4 *cf = reinterpret_cast<const float4 *>(fl + (1 + warp) * Q + 32 * q);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float4 c = cf[i];
-                            float m[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) m[k] *= rf * __uint_as_float(v[4 * i + k]);
-                            hi[2 * i] = take_part(m[0], m[1]);
-                            hi[2 * i + 1] = take_part(m[2], m[3]);
-                            lo[2 * i] = last_part(m[0], m[1]);
-                            lo[2 * i + 1] = last_part(m[2], m[3]);
-                        }
-                    } else {
-                        const float4 *gs = reinterpret_cast<const float4 *>(fl + 32 * q);
-                        const float4 *ds = reinterpret_cast<const float4 *>(fl + Q + 32 * q);
-                        const float gwf = (float)gw;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float4 gv = gs[i], dv = ds[i];
-                            const float ge[4] = {gv.x, gv.y, gv.z, gv.w}, de[4] = {dv.x, dv.y, dv.z, dv.w};
-                            float m[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float e = ex2(gwf - ge[k]) * de[k] * __uint_as_float(v[4 * i + k]);
-                                m[k] = 4 * i + k <= lane ? e : 0.0f;
-                            }
-                            hi[2 * i] = take_part(m[0], m[1]);
-                            hi[2 * i + 1] = take_part(m[2], m[3]);
-                            lo[2 * i] = last_part(m[0], m[1]);
-                            lo[2 * i + 1] = last_part(m[2], m[3]);
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        v[i] = hi[i];
-                        v[16 + i] = lo[i];
-                    }
+                        for (int part = 0; part < 2; ++part)
+                            mma_ts(tm + kColY, tm + 32 * (k >> 1) + 16 * part + 8 * (k & 1), xd + step_mn(k),
+                                   idesc(PW, 0, 1), 1);
+                    umma_commit(&fx.bar[1]);
                 }
-                tmem_st_32x32b_x32(tl + 32 * q, v);
+                const uint64_t bd = desc_mn(sm + kOffB), wd = desc_mn(sm + kOffXw);
+#pragma unroll
+                for (int part = 0; part < 3; ++part)
+#pragma unroll
+                    for (int k = 0; k < Q / 16; ++k)
+                        mma_ss(tm + kColS, bd + step_mn(k), wd + (part * kBlk >> 4) + step_mn(k), idesc(PW, 1, 1),
+                               part + k > 0);
+                umma_commit(&fx.bar[2]);
+                if (tma && t0 + Q < t_end) {
+                    if (!mbar_wait_bounded(&fx.bar[2], parity, nullptr)) fx.bad = 1;
+                    load_bc(t0 + Q);
+                }
             }
-            tmem_st_wait();
+            __syncwarp();
         }
-        fence_async_smem();
-        tc_fence_before();
-        __syncthreads();
-        if (r == 0) {
-            tc_fence_after();
-            if (FULL) {
-                const uint64_t xd = desc_mn(sm + kOffX);
-#pragma unroll
-                for (int k = 0; k < Q / 16; ++k)
-#pragma unroll
-                    for (int part = 0; part < 2; ++part)
-                        mma_ts(tm + kColY, tm + 32 * (k >> 1) + 16 * part + 8 * (k & 1), xd + (k * 256 >> 4),
-                               idesc(PW, 0, 1), 1);
-                umma_commit(&fx.bar[1]);
+    } else {
+        const bf16 *xp = static_cast<const bf16 *>(a.x) + (int64_t)h * a.dv + c0;
+        const bf16 *dp = static_cast<const bf16 *>(a.dt) + h;
+        const float A2 = a.A[h] * 1.4426950408889634f;   // log2 decay per unit step
+        const float Dh = a.D ? a.D[h] : 0.0f, bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
+        const int ti = threadIdx.x % kNT;
+        if (DK < 128) {   // B^T has 128 rows: the missing key rows are zero
+            for (int i = ti; i < kBlk / 16; i += kNT)
+                reinterpret_cast<uint4 *>(sm + kOffB + kBlk)[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        // A token's step and log2 decay, floored at -150 (a factor FP32 flushes to
+        // 0) so that no difference of sums is inf - inf; a NaN passes the comparison by.
+        auto raw_step = [&](int t) {
+            return t < p.len ? __bfloat162float(dp[(p.row0 + (int64_t)t * p.step) * a.lddt]) : 0.0f;
+        };
+        float d;
+        double gw;   // log2 decay up to this token within its warp's 32
+        auto scan_steps = [&](float raw, int t) {
+            d = 0.0f;
+            float l = 0.0f;
+            if (t < p.len) {
+                d = raw + bias;
+                if (a.softplus) d = softplus_f(d);
+                l = d * A2;
+                if (l < -150.0f) l = -150.0f;
             }
-            const uint64_t bd = desc_mn(sm + kOffB), wd = desc_mn(sm + kOffXw);
+            gw = l;
 #pragma unroll
-            for (int part = 0; part < 3; ++part)
-#pragma unroll
-                for (int k = 0; k < Q / 16; ++k)
-                    mma_ss(tm + kColS, bd + (k * 256 >> 4), wd + ((part * 16384 + k * 256) >> 4), idesc(PW, 1, 1),
-                           part + k > 0);
-            umma_commit(&fx.bar[2]);
+            for (int m = 1; m < 32; m <<= 1) {
+                const double o = __shfl_up_sync(0xffffffffu, gw, m);
+                if (lane >= m) gw += o;
+            }
+            if (half == 0 && lane == 31) fx.wsum[warp] = gw;
+        };
+
+        // The state's key row r, this thread's columns.
+        float S[HW];
+        const int64_t soff = ((int64_t)h * DK + r) * a.dv + c0 + half * HW, sall = (int64_t)a.H * DK * a.dv;
+        const float *S0 = nullptr;
+        if (FULL && !idle && r < DK) {
+            if (split && p.n > 1) S0 = a.ws + p.id * sall + soff;
+            else if (a.S0) S0 = a.S0 + p.b * sall + soff;
         }
-        if (FULL) {
-            if (!mbar_wait_bounded(&fx.bar[1], parity, nullptr)) fx.bad = 1;
+#pragma unroll
+        for (int i = 0; i < HW / 4; ++i) {
+            const float4 v = S0 ? reinterpret_cast<const float4 *>(S0)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+            S[4 * i] = v.x; S[4 * i + 1] = v.y; S[4 * i + 2] = v.z; S[4 * i + 3] = v.w;
+        }
+        auto split_state = [&]() {   // the state's two parts
+            if (FULL && r < DK) {
+#pragma unroll
+                for (int j = 0; j < HW / 8; ++j) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float v0 = S[8 * j + 2 * k], v1 = S[8 * j + 2 * k + 1];
+                        hi[k] = take_part(v0, v1);
+                        lo[k] = last_part(v0, v1);
+                    }
+                    *chunk(sm + kOffS, r, half * (HW / 8) + j) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *chunk(sm + kOffS + kBlk, r, half * (HW / 8) + j) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+            }
+        };
+        if (t_first < t_end) {
+            if (ti < 2 * PW) (&fx.first[0][0])[ti] = Q;
+            if (ti < 2) fx.nf[ti] = 0;
+            scan_steps(raw_step(t_first + r), t_first + r);
+            split_state();
+            // half a chunk behind the first group
+            if (grp == 1) asm volatile("bar.sync 5, %0;" ::"n"(2 * kNT) : "memory");
+        }
+        double gsum = 0.0;   // log2 decay of the piece so far
+        for (int t0 = t_first; t0 < t_end; t0 += Q, parity ^= 1) {
+            fence_async_smem();
+            tc_fence_before();
+            sync_all();   // the chunk before is done with shared and tensor memory
+            if (fx.bad) break;
+            const float raw = raw_step(t0 + Q + r);   // the next chunk's step
+            if (ti < PW) fx.first[parity ^ 1][ti] = Q;
+            if (ti == 0) fx.nf[parity ^ 1] = 0;
+            double base = 0.0, total = 0.0;   // before this warp's tokens, and of the chunk
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                if (w < warp) base += fx.wsum[w];
+                total += fx.wsum[w];
+            }
+            const double gt = base + gw;
+            const float wr = d * exp2f((float)(total - gt));   // weight of this token in the next state
+            float fac[3];   // 2^(sum to the end of tokens 32 w .. - g_s) d_s for the rows of later warps
+            if (FULL && half == 1) {
+                double end = 0.0;
+#pragma unroll
+                for (int w = 0; w < 3; ++w) {
+                    end += fx.wsum[w];
+                    fac[w] = d * exp2f((float)(end - gt));
+                }
+            }
+            if (tma) {
+                if (!mbar_wait_bounded(&fx.bar[3], parity, nullptr)) fx.bad = 1;
+                __syncwarp();
+                if (t0 + Q > p.len) {
+                    // a packed sequence's last tile continues into the next sequence
+                    if (t0 + r >= p.len) {
+                        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                        for (int j = 0; j < DK / 16; ++j) {
+                            *chunk(sm + kOffB, r, half * (DK / 16) + j) = zero;
+                            if (FULL) *chunk(sm + kOffC, r, half * (DK / 16) + j) = zero;
+                        }
+#pragma unroll
+                        for (int j = 0; j < PW / 16; ++j) *chunk(sm + kOffX, r, half * (PW / 16) + j) = zero;
+                    }
+                    fence_async_smem();
+                    sync_all();
+                }
+            } else {
+                copy_tile(sm + kOffB, DK / 8, static_cast<const bf16 *>(a.Bm) + g * DK, a.ldb, p, t0, ti);
+                copy_tile(sm + kOffX, PW / 8, xp, a.ldx, p, t0, ti);
+                if (FULL) copy_tile(sm + kOffC, DK / 8, static_cast<const bf16 *>(a.Cm) + g * DK, a.ldc, p, t0, ti);
+                fence_async_smem();
+                sync_all();
+            }
+            if (FULL && !mbar_wait_bounded(&fx.bar[0], parity, nullptr)) fx.bad = 1;
             __syncwarp();
             tc_fence_after();
-            const bool live = t0 + r < p.len;
-            bf16 *yp = static_cast<bf16 *>(a.y) + (p.row0 + (live ? t0 + r : t0) * p.step) * a.ldy +
-                       (int64_t)h * a.dv + c0;
-            const bool nf = fx.nf != 0;
+            float *fl = reinterpret_cast<float *>(sm + kOffF);   // [Q] sums within the warp, [Q] d, [3][Q] factors
+            if (FULL) {
+                if (half == 0) {
+                    fl[r] = (float)gw;
+                    fl[Q + r] = d;
+                } else {
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                uint32_t v[32];
-                tmem_ld_32x32b<32>(tl + kColY + 32 * q, v);
+                    for (int w = 0; w < 3; ++w)
+                        if (w >= warp) fl[(2 + w) * Q + r] = fac[w];
+                }
+            }
+            // X' of this token in three parts; a non-finite x leaves X (times 0 it
+            // would reach earlier tokens) and is marked instead.
+#pragma unroll
+            for (int i = 0; i < HW / 8; ++i) {
+                const int j = half * (HW / 8) + i;
+                Raw<bf16, 8> rx;
+                rx.a = *chunk(sm + kOffX, r, j);
+                float f[8];
+                rx.get(f);
+                uint32_t w[3][4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float v0 = wr * f[2 * k], v1 = wr * f[2 * k + 1];
+                    w[0][k] = take_part(v0, v1);
+                    w[1][k] = take_part(v0, v1);
+                    w[2][k] = last_part(v0, v1);
+                }
+#pragma unroll
+                for (int q = 0; q < 3; ++q)
+                    *chunk(sm + kOffXw + q * kBlk, r, j) = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
+                if (FULL) {
+                    const uint32_t wd[4] = {rx.a.x, rx.a.y, rx.a.z, rx.a.w};
+                    __nv_bfloat162 n = __float2bfloat162_rn(0.0f);   // 0 x finite = 0, else NaN
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        n = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&wd[k]), __float2bfloat162_rn(0.0f), n);
+                    if (*reinterpret_cast<const uint32_t *>(&n) & 0x7fff7fffu) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (!isfinite(f[k])) {
+                                f[k] = 0.0f;
+                                atomicMin(&fx.first[parity][8 * j + k], r);
+                            }
+                        rx.set(f);
+                        *chunk(sm + kOffX, r, j) = rx.a;
+                        fx.nf[parity] = 1;
+                    }
+                }
+            }
+            __syncwarp();
+            if (FULL) {
+                const float et = ex2((float)gt);   // 2^(g_t), on the sum of C S's parts
+                {
+                    uint32_t v[HW], v2[HW];
+                    tmem_ld_32x32b<HW>(tl + kColY + half * HW, v);
+                    tmem_ld_32x32b<HW>(tl + kColS + half * HW, v2);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < HW; ++i)
+                        v[i] = __float_as_uint(et * (__uint_as_float(v[i]) + __uint_as_float(v2[i])));
+                    tmem_st_32x32b_x32(tl + kColY + half * HW, v);
+                }
+                sync();   // the factors
+                // M over G, 32 columns at a time: 16 columns of first parts, 16 of
+                // second.  Columns of earlier warps' tokens factor through the
+                // boundary before this warp's, later ones are zero.
+                const float gwf = (float)gw, rf = ex2(gwf);
+                for (int q = half; q < 4; q += 2) {
+                    uint32_t v[32];
+                    if (q > warp) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = 0u;
+                    } else {
+                        tmem_ld_32x32b<32>(tl + 32 * q, v);
+                        tmem_ld_wait();
+                        uint32_t hi[16], lo[16];
+                        if (q < warp) {
+                            const float4 *cf = reinterpret_cast<const float4 *>(fl + (1 + warp) * Q + 32 * q);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float4 c = cf[i];
+                                float m[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) m[k] *= rf * __uint_as_float(v[4 * i + k]);
+                                hi[2 * i] = take_part(m[0], m[1]);
+                                hi[2 * i + 1] = take_part(m[2], m[3]);
+                                lo[2 * i] = last_part(m[0], m[1]);
+                                lo[2 * i + 1] = last_part(m[2], m[3]);
+                            }
+                        } else {
+                            const float4 *gs = reinterpret_cast<const float4 *>(fl + 32 * q);
+                            const float4 *ds = reinterpret_cast<const float4 *>(fl + Q + 32 * q);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float4 gv = gs[i], dv = ds[i];
+                                const float ge[4] = {gv.x, gv.y, gv.z, gv.w}, de[4] = {dv.x, dv.y, dv.z, dv.w};
+                                float m[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const float e = ex2(gwf - ge[k]) * de[k] * __uint_as_float(v[4 * i + k]);
+                                    m[k] = 4 * i + k <= lane ? e : 0.0f;
+                                }
+                                hi[2 * i] = take_part(m[0], m[1]);
+                                hi[2 * i + 1] = take_part(m[2], m[3]);
+                                lo[2 * i] = last_part(m[0], m[1]);
+                                lo[2 * i + 1] = last_part(m[2], m[3]);
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            v[i] = hi[i];
+                            v[16 + i] = lo[i];
+                        }
+                    }
+                    tmem_st_32x32b_x32(tl + 32 * q, v);
+                }
+                tmem_st_wait();
+            }
+            fence_async_smem();
+            tc_fence_before();
+            sync_all();
+            if (t0 == t_first && grp == 0 && u + 1 < units)
+                asm volatile("bar.arrive 5, %0;" ::"n"(2 * kNT) : "memory");
+            const float keep = exp2f((float)total);
+            gsum += total;
+            if (t0 + Q < t_end) scan_steps(raw, t0 + Q + r);
+            if (FULL) {
+                if (!mbar_wait_bounded(&fx.bar[1], parity, nullptr)) fx.bad = 1;
+                __syncwarp();
+                tc_fence_after();
+                const bool live = t0 + r < p.len;
+                bf16 *yp = static_cast<bf16 *>(a.y) + (p.row0 + (int64_t)(live ? t0 + r : t0) * p.step) * a.ldy +
+                           (int64_t)h * a.dv + c0 + half * HW;
+                const bool nf = fx.nf[parity] != 0;
+                uint32_t v[HW];
+                tmem_ld_32x32b<HW>(tl + kColY + half * HW, v);
                 tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < HW / 8; ++j) {
                     Raw<bf16, 8> rx;
-                    rx.a = *reinterpret_cast<const uint4 *>(sm + kOffX + (4 * q + j) * kChunkB + r * 16);
+                    rx.a = *chunk(sm + kOffX, r, half * (HW / 8) + j);
                     float f[8];
                     rx.get(f);
 #pragma unroll
@@ -413,11 +531,11 @@ __global__ void __launch_bounds__(kNT, 2) ssm_umma_kernel(SsmArgs a, int seg, in
                     if (nf)
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
-                            if (fx.first[32 * q + 8 * j + k] <= r) f[k] = __int_as_float(0x7fffffff);
+                            if (fx.first[parity][half * HW + 8 * j + k] <= r) f[k] = __int_as_float(0x7fffffff);
                     rx.set(f);
                     if (live) {
-                        bf16 *dst = yp + 32 * q + 8 * j;
-                        if (vec) {
+                        bf16 *dst = yp + 8 * j;
+                        if (tma) {
                             rx.store(dst);
                         } else {
                             const uint32_t w[4] = {rx.a.x, rx.a.y, rx.a.z, rx.a.w};
@@ -431,65 +549,95 @@ __global__ void __launch_bounds__(kNT, 2) ssm_umma_kernel(SsmArgs a, int seg, in
                     }
                 }
             }
-        }
-        if (!mbar_wait_bounded(&fx.bar[2], parity, nullptr)) fx.bad = 1;
-        __syncwarp();
-        tc_fence_after();
-        const float keep = exp2f((float)total);
-        gsum += total;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            uint32_t v[32];
-            tmem_ld_32x32b<32>(tl + kColS + 32 * q, v);
+            if (!mbar_wait_bounded(&fx.bar[2], parity, nullptr)) fx.bad = 1;
+            __syncwarp();
+            tc_fence_after();
+            uint32_t v[HW];
+            tmem_ld_32x32b<HW>(tl + kColS + half * HW, v);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) S[32 * q + i] = fmaf(keep, S[32 * q + i], __uint_as_float(v[i]));
+            for (int i = 0; i < HW; ++i) S[i] = fmaf(keep, S[i], __uint_as_float(v[i]));
+            split_state();
         }
+        sync();
+        // A wait that ran out leaves no state that looks like one.
+        if (fx.bad)
+#pragma unroll
+            for (int i = 0; i < HW; ++i) S[i] = __int_as_float(0x7fffffff);
+        if (!idle && r < DK && (!FULL || p.j == p.n - 1)) {
+            float *so = FULL ? a.S_out + p.b * sall + soff : a.ws + p.id * sall + soff;
+#pragma unroll
+            for (int i = 0; i < HW / 4; ++i)
+                reinterpret_cast<float4 *>(so)[i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+        }
+        if (!FULL && !idle && ti == 0 && c0 == 0) ssm_decays(a, seg)[p.id * a.H + h] = exp2f((float)gsum);
     }
     tc_fence_before();
     __syncthreads();
-    // A wait that ran out leaves no state that looks like one.
-    if (fx.bad)
-#pragma unroll
-        for (int i = 0; i < PW; ++i) S[i] = __int_as_float(0x7fffffff);
-    if (r < DK && (!FULL || p.j == p.n - 1)) {
-        float *so = FULL ? a.S_out + p.b * sall + soff : a.ws + z * sall + soff;
-#pragma unroll
-        for (int i = 0; i < PW / 4; ++i)
-            reinterpret_cast<float4 *>(so)[i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
-    }
-    if (!FULL && r == 0 && c0 == 0) ssm_decays(a, seg)[(int64_t)z * a.H + h] = exp2f((float)gsum);
-    if (warp == 0) {
+    if (wid == 0) {
         tmem_relinquish();
-        tmem_dealloc(fx.tmem, kTmemCols);
+        tmem_dealloc(tmem, 2 * kTmemCols);
     }
 }
 
+// cuTensorMapEncodeTiled from the driver, looked up once.
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        const bool ok = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+                        q == cudaDriverEntryPointSuccess;
+        return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p) : nullptr;
+    }();
+    return fn;
+}
+
+bool encode(CUtensorMap *m, const void *base, const Rows &r, int64_t width, int64_t ld) {
+    const auto enc = encoder();
+    if (!enc) return false;
+    const bool packed = r.cu != nullptr;
+    const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)(packed ? 1 : r.B),
+                                (cuuint64_t)(packed ? r.rows : r.rows / r.B)};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * 2 * (packed ? 1 : r.B)};
+    const cuuint32_t box[3] = {64, 1, Q}, es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int DK>
-cudaError_t launch(const SsmArgs &a, int seg, int vec, int split, cudaStream_t s) {
+cudaError_t launch(const SsmArgs &a, const SsmMaps &maps, int seg, int tma, int split, cudaStream_t s) {
+    constexpr int bytes = 2 * (kSmem + (int)sizeof(Fixed));
+    static_assert(bytes <= 226 * 1024, "shared memory of one CTA");
     const int units = a.H * (a.dv / PW);
-    const int64_t grid = piece_count(a.r, seg) * units;
-    cudaError_t e = cudaFuncSetAttribute(ssm_umma_kernel<true, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    const int64_t pairs = (units + 1) / 2;
+    cudaError_t e = cudaFuncSetAttribute(ssm_umma_kernel<true, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     if (split) {
-        e = cudaFuncSetAttribute(ssm_umma_kernel<false, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        e = cudaFuncSetAttribute(ssm_umma_kernel<false, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
-        ssm_umma_kernel<false, DK><<<(unsigned)grid, kNT, kSmem, s>>>(a, seg, units, vec, split);
+        ssm_umma_kernel<false, DK><<<(unsigned)(cut_count(a.r, seg) * pairs), kThreadsAll, bytes, s>>>(a, maps, seg, units,
+                                                                                                tma, split);
         e = launch_ssm_join(a, seg, s);
         if (e != cudaSuccess) return e;
     }
-    ssm_umma_kernel<true, DK><<<(unsigned)grid, kNT, kSmem, s>>>(a, seg, units, vec, split);
+    ssm_umma_kernel<true, DK><<<(unsigned)(piece_count(a.r, seg) * pairs), kThreadsAll, bytes, s>>>(a, maps, seg, units,
+                                                                                              tma, split);
     return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_ssm_umma(const SsmArgs &a, int seg, bool split, cudaStream_t s) {
-    // 16-byte copies need every row to start on a 16-byte boundary.
+    // Tensor copies and 16-byte stores need every row on a 16-byte boundary.
     const uintptr_t base = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.Bm) |
                            reinterpret_cast<uintptr_t>(a.Cm) | reinterpret_cast<uintptr_t>(a.y);
-    const int vec = base % 16 == 0 && a.ldx % 8 == 0 && a.ldb % 8 == 0 && a.ldc % 8 == 0 && a.ldy % 8 == 0;
-    return a.dk == 64 ? launch<64>(a, seg, vec, split, s) : launch<128>(a, seg, vec, split, s);
+    SsmMaps maps{};
+    const bool tma = base % 16 == 0 && a.ldx % 8 == 0 && a.ldb % 8 == 0 && a.ldc % 8 == 0 && a.ldy % 8 == 0 &&
+                     encode(&maps.x, a.x, a.r, (int64_t)a.H * a.dv, a.ldx) &&
+                     encode(&maps.b, a.Bm, a.r, (int64_t)a.G * a.dk, a.ldb) &&
+                     encode(&maps.c, a.Cm, a.r, (int64_t)a.G * a.dk, a.ldc);
+    return a.dk == 64 ? launch<64>(a, maps, seg, tma, split, s) : launch<128>(a, maps, seg, tma, split, s);
 }
 
 }  // namespace lq
