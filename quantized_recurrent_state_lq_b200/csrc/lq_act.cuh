@@ -26,7 +26,7 @@ template <> __device__ __forceinline__ float from_f<float>(float v) { return v; 
 template <> __device__ __forceinline__ bf16 from_f<bf16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ f16 from_f<f16>(float v) { return __float2half_rn(v); }
 
-// V consecutive elements as stored (V = 8: 16-byte accesses, V = 1: one element).
+// V consecutive elements as stored (V = 8 and 4: vector accesses, V = 1: one element).
 template <typename T, int V>
 struct Raw;
 template <typename T>
@@ -37,6 +37,48 @@ struct Raw<T, 1> {
     __device__ __forceinline__ void zero() { v = from_f<T>(0.0f); }
     __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = to_f<T>(v); }
     __device__ __forceinline__ void set(const float (&f)[1]) { v = from_f<T>(f[0]); }
+};
+template <>
+struct Raw<float, 4> {
+    float4 a;
+    __device__ __forceinline__ void load(const float *p) { a = *reinterpret_cast<const float4 *>(p); }
+    __device__ __forceinline__ void store(float *p) const { *reinterpret_cast<float4 *>(p) = a; }
+    __device__ __forceinline__ void zero() { a = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void get(float (&f)[4]) const { f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; }
+    __device__ __forceinline__ void set(const float (&f)[4]) { a = make_float4(f[0], f[1], f[2], f[3]); }
+};
+template <>
+struct Raw<bf16, 4> {
+    uint2 a;
+    __device__ __forceinline__ void load(const bf16 *p) { a = *reinterpret_cast<const uint2 *>(p); }
+    __device__ __forceinline__ void store(bf16 *p) const { *reinterpret_cast<uint2 *>(p) = a; }
+    __device__ __forceinline__ void zero() { a = make_uint2(0u, 0u); }
+    __device__ __forceinline__ void get(float (&f)[4]) const {
+        f[0] = __uint_as_float(a.x << 16);
+        f[1] = __uint_as_float(a.x & 0xffff0000u);
+        f[2] = __uint_as_float(a.y << 16);
+        f[3] = __uint_as_float(a.y & 0xffff0000u);
+    }
+    __device__ __forceinline__ void set(const float (&f)[4]) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(f[0], f[1]), q = __floats2bfloat162_rn(f[2], f[3]);
+        a = make_uint2(*reinterpret_cast<const uint32_t *>(&p), *reinterpret_cast<const uint32_t *>(&q));
+    }
+};
+template <>
+struct Raw<f16, 4> {
+    uint2 a;
+    __device__ __forceinline__ void load(const f16 *p) { a = *reinterpret_cast<const uint2 *>(p); }
+    __device__ __forceinline__ void store(f16 *p) const { *reinterpret_cast<uint2 *>(p) = a; }
+    __device__ __forceinline__ void zero() { a = make_uint2(0u, 0u); }
+    __device__ __forceinline__ void get(float (&f)[4]) const {
+        const float2 u = __half22float2(*reinterpret_cast<const __half2 *>(&a.x));
+        const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&a.y));
+        f[0] = u.x; f[1] = u.y; f[2] = v.x; f[3] = v.y;
+    }
+    __device__ __forceinline__ void set(const float (&f)[4]) {
+        const __half2 p = __floats2half2_rn(f[0], f[1]), q = __floats2half2_rn(f[2], f[3]);
+        a = make_uint2(*reinterpret_cast<const uint32_t *>(&p), *reinterpret_cast<const uint32_t *>(&q));
+    }
 };
 template <>
 struct Raw<float, 8> {
