@@ -158,14 +158,15 @@ __global__ void __launch_bounds__(256) ssm_join_kernel(SsmArgs a, int seg) {
     }
 }
 
-// Tokens per piece.  One CTA takes one piece of 64 value columns of a head and
-// two run on each SM: pieces are cut so that the batch gives about that many.
-// A batch with enough sequences and heads is cut only where a sequence is
-// longer than a CTA's share of all tokens.
-int piece_tokens(const Rows &r, int H, int dv) {
-    const int64_t units = (int64_t)H * dv / 64, slots = 148 * 2;
-    const int64_t share = units <= slots ? (r.rows + slots / units - 1) / (slots / units)
-                                         : (r.rows * units + slots - 1) / slots;
+// Tokens per piece: pieces are cut so that the batch gives about as many
+// workers as the GPU runs side by side -- `workers` per piece (bf16: 64 value
+// columns of a head, two to an SM; else a head, two CTAs to an SM).  A batch
+// with enough sequences and heads is cut only where a sequence is longer than
+// a worker's share of all tokens.
+int piece_tokens(const Rows &r, int dtype, int H, int dv) {
+    const int64_t workers = dtype == kBF16 ? (int64_t)H * dv / 64 : H, slots = 148 * 2;
+    const int64_t share = workers <= slots ? (r.rows + slots / workers - 1) / (slots / workers)
+                                           : (r.rows * workers + slots - 1) / slots;
     const int64_t seg = (share + 127) / 128 * 128;
     return (int)(seg < 128 ? 128 : seg > (1 << 30) ? (1 << 30) : seg);
 }
@@ -181,19 +182,23 @@ cudaError_t launch_ssm_join(const SsmArgs &a, int seg, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+// A prompt whose sequences are this short runs token by token: a chunk costs
+// about as much (10 us) whatever it holds, a token 0.5 us.
+constexpr int kShort = 16;
+
 size_t ssm_ws_bytes(int dtype, int B, int rows, int H, int G, int dk, int dv) {
-    if (dtype != kBF16) return 0;
     Rows r{nullptr, B, rows};
-    const int seg = piece_tokens(r, H, dv);
+    const int seg = piece_tokens(r, dtype, H, dv);
     if (rows <= seg) return 0;
     // packed: at most rows / seg + B pieces, no fewer than time-major ones
     return ((size_t)(rows / seg + B) * H * (dk * dv + 1) * 4 + 255) / 256 * 256;
 }
 
 cudaError_t launch_ssm_prefill(const SsmArgs &a, int dtype, cudaStream_t s) {
-    if (dtype != kBF16 || a.r.rows <= 0) return launch_ssm_step(a, dtype, s);
-    const int seg = piece_tokens(a.r, a.H, a.dv);
-    return launch_ssm_umma(a, seg, may_split(a.r, seg), s);
+    if ((a.r.cu ? a.r.rows : a.r.rows / a.r.B) <= kShort) return launch_ssm_step(a, dtype, s);
+    const int seg = piece_tokens(a.r, dtype, a.H, a.dv);
+    if (dtype == kBF16) return launch_ssm_umma(a, seg, may_split(a.r, seg), s);
+    return launch_ssm_tc(a, dtype, seg, may_split(a.r, seg), s);
 }
 
 }  // namespace lq

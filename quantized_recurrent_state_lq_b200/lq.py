@@ -483,20 +483,20 @@ def _layer_call(fn):
     return call
 
 
-def _have(t, name: str, dtype, dev: int, shape):
+def _refuse(t, name: str, shape, dtype, dev: int):
     if not isinstance(t, torch.Tensor) or t.get_device() != dev:
         raise TypeError(f"{name} must be a CUDA tensor on device {dev}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
 def _rows(t, name: str, shape, n_tail: int, width: int, dtype, dev: int):
     """Pointer and row stride of a tensor of token rows: its last n_tail
     dimensions are one contiguous row of `width` elements, the others evenly
     spaced rows."""
-    _have(t, name, dtype, dev, shape)
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        _refuse(t, name, shape, dtype, dev)
     if t.is_contiguous():
         return t.data_ptr(), width
     st = t.stride()
@@ -522,7 +522,8 @@ def _flat(t, name: str, shape, dev: int, dtype=torch.float32):
     """Pointer of an optional contiguous tensor."""
     if t is None:
         return None
-    _have(t, name, dtype, dev, shape)
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        _refuse(t, name, shape, dtype, dev)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
