@@ -166,6 +166,28 @@ __device__ __forceinline__ float silu_f(float x) {
     return x * sigmoid_f<false>(x);
 }
 
+__device__ __forceinline__ float ex2_f(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float rcp_f(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Two at once, the products and the sum as packed instructions.
+template <bool EXACT>
+__device__ __forceinline__ float2 silu2_f(float2 x) {
+    if constexpr (EXACT) return make_float2(silu_f<true>(x.x), silu_f<true>(x.y));
+    const float l = -1.4426950408889634f;
+    const float2 t = __fmul2_rn(x, make_float2(l, l));
+    const float2 d = __fadd2_rn(make_float2(ex2_f(t.x), ex2_f(t.y)), make_float2(1.0f, 1.0f));
+    return __fmul2_rn(x, make_float2(rcp_f(d.x), rcp_f(d.y)));
+}
+
 // log(1 + e^x) without overflow: max(x, 0) + log1p(e^-|x|).  A NaN passes
 // through (fmaxf alone would drop it).
 __device__ __forceinline__ float softplus_f(float x) {
@@ -190,6 +212,24 @@ struct Piece {
 
 __device__ __forceinline__ int cu_at(const Rows &r, int i) { return min(max(r.cu[i], 0), r.rows); }
 
+// The last sequence b with floor(cu[b] / seg) + add b <= id (0 if none): each
+// lane of the warp probes one of 32 places of what is left, so B sequences
+// take log32(B) dependent loads.  All lanes call it with the same arguments.
+__device__ __forceinline__ int last_sequence(const Rows &r, int seg, int add, int id) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, n = r.B;
+    while (n > 1) {
+        const int step = (n + 31) / 32, at = lo + lane * step;
+        const bool le = at < lo + n && cu_at(r, at) / seg + add * at <= id;
+        const int k = 31 - __clz((int)(__ballot_sync(0xffffffffu, le) | 1u));
+        const int end = lo + n;
+        lo += k * step;
+        n = min(step, end - lo);
+    }
+    return lo;
+}
+
+// (Called by whole warps, every lane with the same id.)
 __device__ __forceinline__ bool find_piece(const Rows &r, int seg, int id, Piece &p) {
     p.id = id;
     if (!r.cu) {
@@ -201,15 +241,10 @@ __device__ __forceinline__ bool find_piece(const Rows &r, int seg, int id, Piece
         p.step = r.B;
         return p.b < r.B;
     }
-    int lo = 0, hi = r.B - 1;   // the last b whose first number is <= id
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (cu_at(r, mid) / seg + mid <= id) lo = mid;
-        else hi = mid - 1;
-    }
-    const int c0 = cu_at(r, lo), c1 = max(cu_at(r, lo + 1), c0);
-    p.b = lo;
-    p.j = id - (c0 / seg + lo);
+    const int b = last_sequence(r, seg, 1, id);
+    const int c0 = cu_at(r, b), c1 = max(cu_at(r, b + 1), c0);
+    p.b = b;
+    p.j = id - (c0 / seg + b);
     p.len = c1 - c0;
     p.n = max(1, (p.len + seg - 1) / seg);
     p.row0 = c0;
@@ -226,14 +261,8 @@ __device__ __forceinline__ bool find_cut(const Rows &r, int seg, int k, Piece &p
         const int b = k / cuts;
         return b < r.B && find_piece(r, seg, b * (cuts + 1) + k % cuts, p);
     }
-    int lo = 0, hi = r.B - 1;   // the last b whose first number is <= k
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (cu_at(r, mid) / seg <= k) lo = mid;
-        else hi = mid - 1;
-    }
-    const int first = cu_at(r, lo) / seg;
-    return k >= first && find_piece(r, seg, k + lo, p) && p.b == lo && p.j < p.n - 1;
+    const int b = last_sequence(r, seg, 0, k);
+    return k >= cu_at(r, b) / seg && find_piece(r, seg, k + b, p) && p.b == b && p.j < p.n - 1;
 }
 
 __host__ __device__ inline int64_t piece_count(const Rows &r, int seg) {

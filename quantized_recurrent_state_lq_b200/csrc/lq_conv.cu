@@ -8,18 +8,19 @@
 // kRun tokens of one sequence for 4 channels (one for widths or rows whose
 // alignment does not allow that): 4 channels keep a warp's accesses whole lines
 // at 4 K weights in registers, half the registers and twice the warps of 8
-// channels (119 us against 57 us for 32768 x 2304 bf16).  It loads kAhead rows before
-// it uses them and keeps the K-1 inputs behind in registers, so an input is
-// read once plus K-1 halo rows per run.  Sums are FP32, the output is rounded
+// channels (119 us against 66 us for 32768 x 2304 bf16).  The next kAhead rows
+// are on their way while one batch is at work, and the K-1 inputs behind stay
+// in registers, so an input is read once plus K-1 halo rows per run.  Sums are FP32, the output is rounded
 // once; the window holds the inputs as they came.
 #include "lq_act.cuh"
+#include "lq_common.cuh"
 
 namespace lq {
 namespace {
 
 constexpr int kConvThreads = 128;
-constexpr int kRun = 64;      // tokens per piece: halo (K-1)/64 more reads, mostly L2 hits
-constexpr int kAhead = 8;     // rows loaded before they are used
+constexpr int kRun = 32;      // tokens per piece: halo (K-1)/32 more reads, mostly L2 hits
+constexpr int kAhead = 4;     // rows loaded ahead of the rows at work
 constexpr int kSeqs = 4;      // sequences of one thread's batch in a step
 
 // The K taps and the bias of V channels (V = 4: w and bias 16-byte aligned).
@@ -45,13 +46,31 @@ __device__ __forceinline__ void load_taps(const ConvArgs &a, int c, float (&w)[V
     }
 }
 
-template <typename T>
-__device__ __forceinline__ float conv_act(float v, int act) {
-    return act ? silu_f<sizeof(T) == 4>(v) : v;
+// act(bias + sum of the taps over rows x[0 .. K-1]) of V channels, two channels
+// per instruction where there are four.
+template <typename T, int V, int K, int R>
+__device__ __forceinline__ void conv_rows(const float (&w)[V][K], const float (&bias)[V], const float (&x)[R][V], int u,
+                                          int act, float (&out)[V]) {
+    if constexpr (V == 4) {
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            float2 s = f2(bias[i], bias[i + 1]);
+#pragma unroll
+            for (int j = 0; j < K; ++j) s = ffma2(f2(w[i][j], w[i + 1][j]), f2(x[u + j][i], x[u + j][i + 1]), s);
+            if (act) s = silu2_f<sizeof(T) == 4>(s);
+            out[i] = s.x;
+            out[i + 1] = s.y;
+        }
+    } else {
+        float s = bias[0];
+#pragma unroll
+        for (int j = 0; j < K; ++j) s = fmaf(w[0][j], x[u + j][0], s);
+        out[0] = act ? silu_f<sizeof(T) == 4>(s) : s;
+    }
 }
 
 template <typename T, int V, int K>
-__global__ void __launch_bounds__(kConvThreads) conv_prefill_kernel(ConvArgs a) {
+__global__ void __launch_bounds__(kConvThreads, sizeof(T) == 4 ? 5 : 8) conv_prefill_kernel(ConvArgs a) {
     const int c = (blockIdx.y * kConvThreads + threadIdx.x) * V;
     Piece p;
     if (!find_piece(a.r, kRun, blockIdx.x, p) || c >= a.C) return;
@@ -86,23 +105,22 @@ __global__ void __launch_bounds__(kConvThreads) conv_prefill_kernel(ConvArgs a) 
     const int64_t dx = p.step * a.ldx, dy = p.step * a.ldy;
     const T *xr = x + (p.row0 + t0 * p.step) * a.ldx;
     T *yr = static_cast<T *>(a.y) + c + (p.row0 + t0 * p.step) * a.ldy;
-    for (int t = t0; t < t1; t += kAhead) {
-        Raw<T, V> raw[kAhead];
+    Raw<T, V> next[kAhead];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-            if (t + u < t1) raw[u].load(xr + u * dx);
+    for (int u = 0; u < kAhead; ++u)
+        if (t0 + u < t1) next[u].load(xr + u * dx);
+    for (int t = t0; t < t1; t += kAhead) {
+        xr += kAhead * dx;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            next[u].get(in[K - 1 + u]);   // (beyond t1: not used)
+            if (t + kAhead + u < t1) next[u].load(xr + u * dx);
+        }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             if (t + u < t1) {
-                raw[u].get(in[K - 1 + u]);
                 float out[V];
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    float s = bias[i];
-#pragma unroll
-                    for (int j = 0; j < K; ++j) s = fmaf(w[i][j], in[u + j][i], s);
-                    out[i] = conv_act<T>(s, a.act);
-                }
+                conv_rows<T, V, K>(w, bias, in, u, a.act, out);
                 Raw<T, V> o;
                 o.set(out);
                 o.store(yr + u * dy);
@@ -112,7 +130,6 @@ __global__ void __launch_bounds__(kConvThreads) conv_prefill_kernel(ConvArgs a) 
         for (int j = 0; j < K - 1; ++j)
 #pragma unroll
             for (int i = 0; i < V; ++i) in[j][i] = in[kAhead + j][i];
-        xr += kAhead * dx;
         yr += kAhead * dy;
     }
 }
@@ -140,18 +157,10 @@ __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(ConvArgs a, int
 #pragma unroll
         for (int u = 0; u < kSeqs; ++u)
             if (b + u < b1) {
-                float out[V];
+                float in[K][V], out[V];
 #pragma unroll
-                for (int i = 0; i < V; ++i) out[i] = bias[i];
-#pragma unroll
-                for (int j = 0; j < K; ++j) {
-                    float f[V];
-                    r[u][j].get(f);
-#pragma unroll
-                    for (int i = 0; i < V; ++i) out[i] = fmaf(w[i][j], f[i], out[i]);
-                }
-#pragma unroll
-                for (int i = 0; i < V; ++i) out[i] = conv_act<T>(out[i], a.act);
+                for (int j = 0; j < K; ++j) r[u][j].get(in[j]);
+                conv_rows<T, V, K>(w, bias, in, 0, a.act, out);
                 Raw<T, V> o;
                 o.set(out);
                 o.store(static_cast<T *>(a.y) + (b + u) * a.ldy + c);

@@ -14,10 +14,9 @@
 //
 // A group of eight warps takes 64 value columns of one head over one piece of
 // a sequence: two threads per token, key row and tensor-memory lane, 32 columns
-// each, and a ninth warp that issues the group's copies and MMAs.  Its phases
-// alternate between the tensor core and the threads, so a CTA runs two groups
-// (256 tensor-memory columns, 112 KB of shared memory each) half a chunk apart:
-// a kernel that uses tensor memory gets one CTA per SM here.
+// each.  Its phases alternate between the tensor core and the threads, so a CTA
+// runs two groups (256 tensor-memory columns, 112 KB of shared memory each)
+// half a chunk apart: a kernel that uses tensor memory gets one CTA per SM here.
 // Long sequences of a small batch are cut into pieces: a first pass forms each
 // piece's own state, ssm_join_kernel chains them, the second pass starts every
 // piece from its state (about a third more work for pieces x as much
@@ -46,8 +45,7 @@ namespace {
 constexpr int Q = 128;                 // tokens per chunk
 constexpr int PW = 64;                 // value columns of a group
 constexpr int HW = PW / 2;             // and of a thread
-constexpr int kNT = 256;               // computing threads of a group
-constexpr int kThreadsAll = 2 * kNT + 64;
+constexpr int kNT = 256;               // threads of a group
 constexpr int kBlk = Q * 128;          // bytes of 128 rows of 64 columns
 constexpr int kOffC = 0, kOffS = 2 * kBlk, kOffXw = 0, kOffF = 3 * kBlk, kOffB = 4 * kBlk, kOffX = 6 * kBlk;
 constexpr int kSmem = 7 * kBlk;
@@ -102,24 +100,29 @@ __device__ __forceinline__ void tma_rows(void *dst, const CUtensorMap *map, int 
         : "memory");
 }
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
 
 // bf16 parts of a pair: returns the pair rounded to bf16 and leaves the rests.
-__device__ __forceinline__ uint32_t take_part(float &a, float &b) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
-    const uint32_t w = *reinterpret_cast<const uint32_t *>(&p);
-    a -= __uint_as_float(w << 16);
-    b -= __uint_as_float(w & 0xffff0000u);
-    return w;
-}
-__device__ __forceinline__ uint32_t last_part(float a, float b) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+__device__ __forceinline__ uint32_t last_part(float2 v) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(v.x, v.y);
     return *reinterpret_cast<const uint32_t *>(&p);
 }
+__device__ __forceinline__ uint32_t take_part(float2 &v) {
+    const uint32_t w = last_part(v);
+    v = ffma2(bf16x2_to_f2(w), f2(-1.0f, -1.0f), v);
+    return w;
+}
+
+__device__ __forceinline__ void tma_store_rows(const CUtensorMap *map, const void *src, int col, int b, int t) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(col), "r"(b), "r"(t), "r"(smem_u32(src))
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// The stores have read their shared memory (done: and written theirs).
+__device__ __forceinline__ void tma_store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // Rows t0 .. t0 + Q - 1 of a sequence (zeros from its end on), NCH chunks of 8
 // elements each, element by element: thread i of the group.
@@ -137,10 +140,10 @@ __device__ __forceinline__ void copy_tile(unsigned char *dst, int nch, const bf1
     }
 }
 
-// Token rows [T][B][width] of x, B and C as 3-D maps, boxes of 64 columns x 128
+// Token rows [T][B][width] of x, B, C and y as 3-D maps, boxes of 64 columns x 128
 // tokens of one sequence (packed: one sequence of all rows).
 struct alignas(64) SsmMaps {
-    CUtensorMap x, b, c;
+    CUtensorMap x, b, c, y;
 };
 
 struct Fixed {
@@ -154,13 +157,12 @@ struct Fixed {
 // FULL: outputs and the final state; else only the pieces' own states (from
 // zero) and decays, for all but the last piece of each sequence.
 template <bool FULL, int DK>
-__global__ void __launch_bounds__(kThreadsAll, 1)
+__global__ void __launch_bounds__(2 * kNT, 1)
     ssm_umma_kernel(SsmArgs a, const __grid_constant__ SsmMaps maps, int seg, int units, int tma, int split) {
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ uint32_t tmem;
     const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool issuer = wid >= 2 * kNT / 32;
-    const int grp = issuer ? wid - 2 * kNT / 32 : threadIdx.x / kNT;
+    const int grp = threadIdx.x / kNT, ti = threadIdx.x % kNT;
     unsigned char *sm = smem + grp * kSmem;
     Fixed &fx = reinterpret_cast<Fixed *>(smem + 2 * kSmem)[grp];
     const int warp = wid & 3, half = (wid >> 2) & 1, r = warp * 32 + lane;   // 32 rows, 32 columns of this warp
@@ -169,99 +171,42 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
     Piece p;
     if (!(FULL ? find_piece(a.r, seg, z, p) : find_cut(a.r, seg, z, p))) return;
     const bool idle = u >= units;   // the second group of an odd number of units
-    // barriers of the group: with its issuing warp, and without
-    auto sync_all = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(kNT + 32) : "memory"); };
-    auto sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(3 + grp), "n"(kNT) : "memory"); };
+    auto sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(kNT) : "memory"); };
     const int per = a.dv / PW;
     const int h = idle ? 0 : u / per, c0 = (u % per) * PW;
     const int g = (int)((int64_t)h * a.G / a.H);
     const int t_first = p.j * seg, t_end = idle ? t_first : min(p.len, t_first + seg);
+    // where TMA finds token t: (row of its sequence, sequence)
+    const int tm_t = a.r.cu ? (int)p.row0 : 0, tm_b = a.r.cu ? 0 : p.b;
+    const bool lead = ti == 0;   // issues the group's copies and MMAs
 
-    if (wid == 0) tmem_alloc(&tmem, 2 * kTmemCols);
-    if (issuer && lane == 0) {
+    // B and C of a chunk (their places are free once B^T X' of the chunk before
+    // is done), then X (free once its outputs are on their way).
+    auto load_bc = [&](int t0) {
+        mbar_arrive_expect_tx(&fx.bar[3], (FULL ? 2 : 1) * (DK / 64) * kBlk + kBlk);
+#pragma unroll
+        for (int j = 0; j < DK / 64; ++j) {
+            tma_rows(sm + kOffB + j * kBlk, &maps.b, g * DK + 64 * j, tm_b, tm_t + t0, &fx.bar[3]);
+            if (FULL) tma_rows(sm + kOffC + j * kBlk, &maps.c, g * DK + 64 * j, tm_b, tm_t + t0, &fx.bar[3]);
+        }
+    };
+    auto load_x = [&](int t0) { tma_rows(sm + kOffX, &maps.x, h * a.dv + c0, tm_b, tm_t + t0, &fx.bar[3]); };
+
+    if (lead) {
         for (int i = 0; i < 4; ++i) mbar_init(&fx.bar[i], 1);
         fx.bad = 0;
         fence_mbar_init();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tm = tmem + grp * kTmemCols, tl = tm + ((uint32_t)warp << 21);   // this warp's lanes: 32 warp
-    int parity = 0;
-
-    if (issuer) {
-        // where TMA finds token t: (row of its sequence, sequence)
-        const int tm_t = a.r.cu ? (int)p.row0 : 0, tm_b = a.r.cu ? 0 : p.b;
-        // B and C of a chunk (their places are free once B^T X' of the chunk
-        // before is done), then X (free once its outputs are written).
-        auto load_bc = [&](int t0) {
-            mbar_arrive_expect_tx(&fx.bar[3], (FULL ? 2 : 1) * (DK / 64) * kBlk + kBlk);
-#pragma unroll
-            for (int j = 0; j < DK / 64; ++j) {
-                tma_rows(sm + kOffB + j * kBlk, &maps.b, g * DK + 64 * j, tm_b, tm_t + t0, &fx.bar[3]);
-                if (FULL) tma_rows(sm + kOffC + j * kBlk, &maps.c, g * DK + 64 * j, tm_b, tm_t + t0, &fx.bar[3]);
-            }
-        };
-        auto load_x = [&](int t0) { tma_rows(sm + kOffX, &maps.x, h * a.dv + c0, tm_b, tm_t + t0, &fx.bar[3]); };
-        if (tma && lane == 0 && t_first < t_end) {
+        if (tma && t_first < t_end) {
             load_bc(t_first);
             load_x(t_first);
         }
-        for (int t0 = t_first; t0 < t_end; t0 += Q, parity ^= 1) {
-            sync_all();   // the chunk before is done with shared and tensor memory
-            if (lane == 0 && tma && t0 != t_first) load_x(t0);
-            if (fx.bad) {
-                if (lane == 0 && tma) mbar_wait_bounded(&fx.bar[3], parity, nullptr);   // the copies under way
-                break;
-            }
-            if (!tma || t0 + Q > p.len) sync_all();   // tiles copied or their ends cleared by the threads
-            if (FULL && lane == 0) {
-                if (tma && !mbar_wait_bounded(&fx.bar[3], parity, nullptr)) fx.bad = 1;
-                tc_fence_after();
-                const uint64_t cd = desc_k(sm + kOffC), bd = desc_k(sm + kOffB), sd = desc_mn(sm + kOffS);
-#pragma unroll
-                for (int k = 0; k < DK / 16; ++k) mma_ss(tm, cd + step_k(k), bd + step_k(k), idesc(Q, 0, 0), k > 0);
-                // C S, its parts side by side: [kColY, kColS) and [kColS, 256)
-#pragma unroll
-                for (int k = 0; k < DK / 16; ++k)
-                    mma_ss(tm + kColY, cd + step_k(k), sd + step_mn(k), idesc(2 * PW, 0, 1), k > 0);
-                umma_commit(&fx.bar[0]);
-            }
-            __syncwarp();
-            sync_all();   // X', M and the scaled C S are in place
-            if (lane == 0) {
-                tc_fence_after();
-                if (FULL) {
-                    const uint64_t xd = desc_mn(sm + kOffX);
-#pragma unroll
-                    for (int k = 0; k < Q / 16; ++k)
-#pragma unroll
-                        for (int part = 0; part < 2; ++part)
-                            mma_ts(tm + kColY, tm + 32 * (k >> 1) + 16 * part + 8 * (k & 1), xd + step_mn(k),
-                                   idesc(PW, 0, 1), 1);
-                    umma_commit(&fx.bar[1]);
-                }
-                const uint64_t bd = desc_mn(sm + kOffB), wd = desc_mn(sm + kOffXw);
-#pragma unroll
-                for (int part = 0; part < 3; ++part)
-#pragma unroll
-                    for (int k = 0; k < Q / 16; ++k)
-                        mma_ss(tm + kColS, bd + step_mn(k), wd + (part * kBlk >> 4) + step_mn(k), idesc(PW, 1, 1),
-                               part + k > 0);
-                umma_commit(&fx.bar[2]);
-                if (tma && t0 + Q < t_end) {
-                    if (!mbar_wait_bounded(&fx.bar[2], parity, nullptr)) fx.bad = 1;
-                    load_bc(t0 + Q);
-                }
-            }
-            __syncwarp();
-        }
-    } else {
+    }
+    if (wid == 1) tmem_alloc(&tmem, 2 * kTmemCols);
+    {
         const bf16 *xp = static_cast<const bf16 *>(a.x) + (int64_t)h * a.dv + c0;
         const bf16 *dp = static_cast<const bf16 *>(a.dt) + h;
         const float A2 = a.A[h] * 1.4426950408889634f;   // log2 decay per unit step
         const float Dh = a.D ? a.D[h] : 0.0f, bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
-        const int ti = threadIdx.x % kNT;
         if (DK < 128) {   // B^T has 128 rows: the missing key rows are zero
             for (int i = ti; i < kBlk / 16; i += kNT)
                 reinterpret_cast<uint4 *>(sm + kOffB + kBlk)[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -311,9 +256,9 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        float v0 = S[8 * j + 2 * k], v1 = S[8 * j + 2 * k + 1];
-                        hi[k] = take_part(v0, v1);
-                        lo[k] = last_part(v0, v1);
+                        float2 v = f2(S[8 * j + 2 * k], S[8 * j + 2 * k + 1]);
+                        hi[k] = take_part(v);
+                        lo[k] = last_part(v);
                     }
                     *chunk(sm + kOffS, r, half * (HW / 8) + j) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *chunk(sm + kOffS + kBlk, r, half * (HW / 8) + j) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -325,15 +270,34 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
             if (ti < 2) fx.nf[ti] = 0;
             scan_steps(raw_step(t_first + r), t_first + r);
             split_state();
-            // half a chunk behind the first group
-            if (grp == 1) asm volatile("bar.sync 5, %0;" ::"n"(2 * kNT) : "memory");
         }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        const uint32_t tm = tmem + grp * kTmemCols, tl = tm + ((uint32_t)warp << 21);   // this warp's lanes: 32 warp
+        int parity = 0;
+        // the second group half a chunk behind the first
+        if (grp == 1 && t_first < t_end) asm volatile("bar.sync 5, %0;" ::"n"(2 * kNT) : "memory");
+        // A chunk's outputs, which are in X's place.
+        auto tma_store = [&](int t0) {
+            if (FULL) {
+                tma_store_rows(&maps.y, sm + kOffX, h * a.dv + c0, tm_b, tm_t + t0);
+                tma_store_read();
+            }
+        };
         double gsum = 0.0;   // log2 decay of the piece so far
         for (int t0 = t_first; t0 < t_end; t0 += Q, parity ^= 1) {
             fence_async_smem();
             tc_fence_before();
-            sync_all();   // the chunk before is done with shared and tensor memory
-            if (fx.bad) break;
+            sync();   // the chunk before is done with shared and tensor memory
+            if (lead && tma && t0 != t_first) {   // its outputs leave, the next X comes
+                tma_store(t0 - Q);
+                load_x(t0);
+            }
+            if (fx.bad) {
+                if (lead && tma) mbar_wait_bounded(&fx.bar[3], parity, nullptr);   // the copies under way
+                break;
+            }
             const float raw = raw_step(t0 + Q + r);   // the next chunk's step
             if (ti < PW) fx.first[parity ^ 1][ti] = Q;
             if (ti == 0) fx.nf[parity ^ 1] = 0;
@@ -370,14 +334,25 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
                         for (int j = 0; j < PW / 16; ++j) *chunk(sm + kOffX, r, half * (PW / 16) + j) = zero;
                     }
                     fence_async_smem();
-                    sync_all();
+                    sync();
                 }
             } else {
                 copy_tile(sm + kOffB, DK / 8, static_cast<const bf16 *>(a.Bm) + g * DK, a.ldb, p, t0, ti);
                 copy_tile(sm + kOffX, PW / 8, xp, a.ldx, p, t0, ti);
                 if (FULL) copy_tile(sm + kOffC, DK / 8, static_cast<const bf16 *>(a.Cm) + g * DK, a.ldc, p, t0, ti);
                 fence_async_smem();
-                sync_all();
+                sync();
+            }
+            if (FULL && lead) {
+                tc_fence_after();
+                const uint64_t cd = desc_k(sm + kOffC), bd = desc_k(sm + kOffB), sd = desc_mn(sm + kOffS);
+#pragma unroll
+                for (int k = 0; k < DK / 16; ++k) mma_ss(tm, cd + step_k(k), bd + step_k(k), idesc(Q, 0, 0), k > 0);
+                // C S, its parts side by side: [kColY, kColS) and [kColS, 256)
+#pragma unroll
+                for (int k = 0; k < DK / 16; ++k)
+                    mma_ss(tm + kColY, cd + step_k(k), sd + step_mn(k), idesc(2 * PW, 0, 1), k > 0);
+                umma_commit(&fx.bar[0]);
             }
             if (FULL && !mbar_wait_bounded(&fx.bar[0], parity, nullptr)) fx.bad = 1;
             __syncwarp();
@@ -405,10 +380,10 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
                 uint32_t w[3][4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    float v0 = wr * f[2 * k], v1 = wr * f[2 * k + 1];
-                    w[0][k] = take_part(v0, v1);
-                    w[1][k] = take_part(v0, v1);
-                    w[2][k] = last_part(v0, v1);
+                    float2 v = mul2(f2(wr, wr), f2(f[2 * k], f[2 * k + 1]));
+                    w[0][k] = take_part(v);
+                    w[1][k] = take_part(v);
+                    w[2][k] = last_part(v);
                 }
 #pragma unroll
                 for (int q = 0; q < 3; ++q)
@@ -434,7 +409,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
             }
             __syncwarp();
             if (FULL) {
-                const float et = ex2((float)gt);   // 2^(g_t), on the sum of C S's parts
+                const float et = ex2_f((float)gt);   // 2^(g_t), on the sum of C S's parts
                 {
                     uint32_t v[HW], v2[HW];
                     tmem_ld_32x32b<HW>(tl + kColY + half * HW, v);
@@ -449,7 +424,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
                 // M over G, 32 columns at a time: 16 columns of first parts, 16 of
                 // second.  Columns of earlier warps' tokens factor through the
                 // boundary before this warp's, later ones are zero.
-                const float gwf = (float)gw, rf = ex2(gwf);
+                const float gwf = (float)gw, rf = ex2_f(gwf);
                 for (int q = half; q < 4; q += 2) {
                     uint32_t v[32];
                     if (q > warp) {
@@ -464,13 +439,15 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
                                 const float4 c = cf[i];
-                                float m[4] = {c.x, c.y, c.z, c.w};
+                                const float2 cc[2] = {f2(c.x, c.y), f2(c.z, c.w)};
 #pragma unroll
-                                for (int k = 0; k < 4; ++k) m[k] *= rf * __uint_as_float(v[4 * i + k]);
-                                hi[2 * i] = take_part(m[0], m[1]);
-                                hi[2 * i + 1] = take_part(m[2], m[3]);
-                                lo[2 * i] = last_part(m[0], m[1]);
-                                lo[2 * i + 1] = last_part(m[2], m[3]);
+                                for (int k = 0; k < 2; ++k) {
+                                    const float2 gg = f2(__uint_as_float(v[4 * i + 2 * k]),
+                                                         __uint_as_float(v[4 * i + 2 * k + 1]));
+                                    float2 m = mul2(cc[k], mul2(f2(rf, rf), gg));
+                                    hi[2 * i + k] = take_part(m);
+                                    lo[2 * i + k] = last_part(m);
+                                }
                             }
                         } else {
                             const float4 *gs = reinterpret_cast<const float4 *>(fl + 32 * q);
@@ -482,13 +459,15 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
                                 float m[4];
 #pragma unroll
                                 for (int k = 0; k < 4; ++k) {
-                                    const float e = ex2(gwf - ge[k]) * de[k] * __uint_as_float(v[4 * i + k]);
+                                    const float e = ex2_f(gwf - ge[k]) * de[k] * __uint_as_float(v[4 * i + k]);
                                     m[k] = 4 * i + k <= lane ? e : 0.0f;
                                 }
-                                hi[2 * i] = take_part(m[0], m[1]);
-                                hi[2 * i + 1] = take_part(m[2], m[3]);
-                                lo[2 * i] = last_part(m[0], m[1]);
-                                lo[2 * i + 1] = last_part(m[2], m[3]);
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    float2 mm = f2(m[2 * k], m[2 * k + 1]);
+                                    hi[2 * i + k] = take_part(mm);
+                                    lo[2 * i + k] = last_part(mm);
+                                }
                             }
                         }
 #pragma unroll
@@ -503,27 +482,64 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
             }
             fence_async_smem();
             tc_fence_before();
-            sync_all();
+            sync();
+            if (lead) {
+                tc_fence_after();
+                const uint64_t bd = desc_mn(sm + kOffB), wd = desc_mn(sm + kOffXw), xd = desc_mn(sm + kOffX);
+#pragma unroll
+                for (int part = 0; part < 3; ++part)
+#pragma unroll
+                    for (int k = 0; k < Q / 16; ++k)
+                        mma_ss(tm + kColS, bd + step_mn(k), wd + (part * kBlk >> 4) + step_mn(k), idesc(PW, 1, 1),
+                               part + k > 0);
+                umma_commit(&fx.bar[2]);
+                if (FULL) {
+#pragma unroll
+                    for (int k = 0; k < Q / 16; ++k)
+#pragma unroll
+                        for (int part = 0; part < 2; ++part)
+                            mma_ts(tm + kColY, tm + 32 * (k >> 1) + 16 * part + 8 * (k & 1), xd + step_mn(k),
+                                   idesc(PW, 0, 1), 1);
+                    umma_commit(&fx.bar[1]);
+                }
+            }
+            __syncwarp();
             if (t0 == t_first && grp == 0 && u + 1 < units)
                 asm volatile("bar.arrive 5, %0;" ::"n"(2 * kNT) : "memory");
             const float keep = exp2f((float)total);
             gsum += total;
             if (t0 + Q < t_end) scan_steps(raw, t0 + Q + r);
+            if (!mbar_wait_bounded(&fx.bar[2], parity, nullptr)) fx.bad = 1;
+            if (lead && tma && t0 + Q < t_end) load_bc(t0 + Q);
+            __syncwarp();
+            tc_fence_after();
+            {
+                uint32_t v[HW];
+                tmem_ld_32x32b<HW>(tl + kColS + half * HW, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < HW; i += 2) {
+                    const float2 s = ffma2(f2(keep, keep), f2(S[i], S[i + 1]),
+                                           f2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
+                    S[i] = s.x;
+                    S[i + 1] = s.y;
+                }
+            }
+            split_state();
             if (FULL) {
+                // outputs into X's place; full tiles leave by a tensor store
                 if (!mbar_wait_bounded(&fx.bar[1], parity, nullptr)) fx.bad = 1;
                 __syncwarp();
                 tc_fence_after();
-                const bool live = t0 + r < p.len;
-                bf16 *yp = static_cast<bf16 *>(a.y) + (p.row0 + (int64_t)(live ? t0 + r : t0) * p.step) * a.ldy +
-                           (int64_t)h * a.dv + c0 + half * HW;
                 const bool nf = fx.nf[parity] != 0;
                 uint32_t v[HW];
                 tmem_ld_32x32b<HW>(tl + kColY + half * HW, v);
                 tmem_ld_wait();
 #pragma unroll
                 for (int j = 0; j < HW / 8; ++j) {
+                    uint4 *at = chunk(sm + kOffX, r, half * (HW / 8) + j);
                     Raw<bf16, 8> rx;
-                    rx.a = *chunk(sm + kOffX, r, half * (HW / 8) + j);
+                    rx.a = *at;
                     float f[8];
                     rx.get(f);
 #pragma unroll
@@ -533,12 +549,20 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
                         for (int k = 0; k < 8; ++k)
                             if (fx.first[parity][half * HW + 8 * j + k] <= r) f[k] = __int_as_float(0x7fffffff);
                     rx.set(f);
-                    if (live) {
-                        bf16 *dst = yp + 8 * j;
+                    *at = rx.a;
+                }
+                if (!tma || t0 + Q > p.len) {   // element by element: unaligned rows, a sequence's last rows
+                    sync();
+                    for (int i = ti; i < Q * (PW / 8); i += kNT) {
+                        const int t = i / (PW / 8), j = i % (PW / 8);
+                        if (t0 + t >= p.len) break;
+                        const uint4 w4 = *chunk(sm + kOffX, t, j);
+                        bf16 *dst = static_cast<bf16 *>(a.y) + (p.row0 + (int64_t)(t0 + t) * p.step) * a.ldy +
+                                    (int64_t)h * a.dv + c0 + 8 * j;
                         if (tma) {
-                            rx.store(dst);
+                            *reinterpret_cast<uint4 *>(dst) = w4;
                         } else {
-                            const uint32_t w[4] = {rx.a.x, rx.a.y, rx.a.z, rx.a.w};
+                            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
                             uint16_t *e = reinterpret_cast<uint16_t *>(dst);
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
@@ -549,17 +573,14 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
                     }
                 }
             }
-            if (!mbar_wait_bounded(&fx.bar[2], parity, nullptr)) fx.bad = 1;
-            __syncwarp();
-            tc_fence_after();
-            uint32_t v[HW];
-            tmem_ld_32x32b<HW>(tl + kColS + half * HW, v);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < HW; ++i) S[i] = fmaf(keep, S[i], __uint_as_float(v[i]));
-            split_state();
         }
+        fence_async_smem();
         sync();
+        const int t_last = t_first + (t_end - t_first - 1) / Q * Q;   // the last chunk
+        if (FULL && lead && tma && t_first < t_end && t_last + Q <= p.len && !fx.bad) {
+            tma_store(t_last);
+            tma_store_done();
+        }
         // A wait that ran out leaves no state that looks like one.
         if (fx.bad)
 #pragma unroll
@@ -574,7 +595,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (wid == 0) {
+    if (wid == 1) {
         tmem_relinquish();
         tmem_dealloc(tmem, 2 * kTmemCols);
     }
@@ -616,12 +637,12 @@ cudaError_t launch(const SsmArgs &a, const SsmMaps &maps, int seg, int tma, int 
     if (split) {
         e = cudaFuncSetAttribute(ssm_umma_kernel<false, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
-        ssm_umma_kernel<false, DK><<<(unsigned)(cut_count(a.r, seg) * pairs), kThreadsAll, bytes, s>>>(a, maps, seg, units,
+        ssm_umma_kernel<false, DK><<<(unsigned)(cut_count(a.r, seg) * pairs), 2 * kNT, bytes, s>>>(a, maps, seg, units,
                                                                                                 tma, split);
         e = launch_ssm_join(a, seg, s);
         if (e != cudaSuccess) return e;
     }
-    ssm_umma_kernel<true, DK><<<(unsigned)(piece_count(a.r, seg) * pairs), kThreadsAll, bytes, s>>>(a, maps, seg, units,
+    ssm_umma_kernel<true, DK><<<(unsigned)(piece_count(a.r, seg) * pairs), 2 * kNT, bytes, s>>>(a, maps, seg, units,
                                                                                               tma, split);
     return cudaGetLastError();
 }
@@ -636,7 +657,8 @@ cudaError_t launch_ssm_umma(const SsmArgs &a, int seg, bool split, cudaStream_t 
     const bool tma = base % 16 == 0 && a.ldx % 8 == 0 && a.ldb % 8 == 0 && a.ldc % 8 == 0 && a.ldy % 8 == 0 &&
                      encode(&maps.x, a.x, a.r, (int64_t)a.H * a.dv, a.ldx) &&
                      encode(&maps.b, a.Bm, a.r, (int64_t)a.G * a.dk, a.ldb) &&
-                     encode(&maps.c, a.Cm, a.r, (int64_t)a.G * a.dk, a.ldc);
+                     encode(&maps.c, a.Cm, a.r, (int64_t)a.G * a.dk, a.ldc) &&
+                     encode(&maps.y, a.y, a.r, (int64_t)a.H * a.dv, a.ldy);
     return a.dk == 64 ? launch<64>(a, maps, seg, tma, split, s) : launch<128>(a, maps, seg, tma, split, s);
 }
 
