@@ -14,6 +14,34 @@ __host__ __device__ inline float *ssm_decays(const SsmArgs &a, int seg) {
     return a.ws + piece_count(a.r, seg) * a.H * a.dk * a.dv;
 }
 
+// Log2 decays and their running sums as fixed point with 32 fraction bits: the
+// sum of a chunk (at most 128 x 150) and every difference are exact to 2^-33 per
+// token, and cost integer adds (FP64 sums took 4000 cycles a chunk here).
+__device__ __forceinline__ long long decay_fix(float l) { return __float2ll_rn(l * 4294967296.0f); }
+__device__ __forceinline__ float decay_f(long long v) {
+    return fmaf((float)(unsigned)v, 0x1p-32f, (float)(int)(v >> 32));
+}
+
+// A token's step d and log2 decay d A: within +-150 (2^-150 is flushed to 0 in
+// FP32, 2^150 is its infinity), so that no difference of sums is inf - inf.  A
+// decay that is not a number makes the step one, which shows in all it touches.
+__device__ __forceinline__ long long decay_of(float &d, float A2) {
+    float l = d * A2;
+    if (l != l) d = l;
+    l = fminf(fmaxf(l, -150.0f), 150.0f);
+    return decay_fix(l);
+}
+
+__device__ __forceinline__ long long warp_scan(long long v) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, v, m);
+        if (lane >= m) v += o;
+    }
+    return v;
+}
+
 // Chain the pieces of every sequence cut in more than one:  S = S0; for each
 // piece, slot <- S and S <- decay S + own.
 cudaError_t launch_ssm_join(const SsmArgs &a, int seg, cudaStream_t s);

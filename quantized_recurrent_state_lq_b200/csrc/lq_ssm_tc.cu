@@ -58,7 +58,7 @@ struct Tiles {
     float B[Q][DK + 4];    // rows 4 banks apart: its columns' fragments without
     float X[Q][DV + 4];    // and the outputs, at the end
     float M[Q][Q + 8];
-    double g[Q];           // log2 decay from the chunk's start
+    long long g[Q];        // log2 decay from the chunk's start (fixed point)
     float d[Q], eg[Q], w[Q];   // steps, 2^g, weights in the next state
     int first[DV];         // per value column, the first token whose x is not finite
     float keep;            // 2^(g_Q)
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(2 * DV, DV == 128 ? 2 : 4) ssm_tc_kernel(SsmAr
 #pragma unroll
         for (int e = 0; e < 4; ++e) S[i][e] = S0 ? S0[(8 * i + 2 * tq + (e & 1)) * DV + (e >> 1) * 8] : 0.0f;
 
-    double gsum = 0.0;
+    long long gsum = 0;
     const int t_end = min(p.len, (p.j + 1) * seg);
     for (int t0 = p.j * seg; t0 < t_end; t0 += Q) {
         __syncthreads();   // the chunk before is done with the tiles
@@ -130,28 +130,20 @@ __global__ void __launch_bounds__(2 * DV, DV == 128 ? 2 : 4) ssm_tc_kernel(SsmAr
         if (FULL) load_rows<T, DK, NT>(s.C, cp, a.ldc, p, t0, vec);
         if (tid < DV) s.first[tid] = Q;
         if (warp == 0) {
-            // This token's step and log2 decay, floored at -150 (a factor FP32
-            // flushes to 0) so that no difference of sums is inf - inf; a NaN
-            // passes the comparison by.
-            float d = 0.0f, l = 0.0f;
+            float d = 0.0f;
+            long long gt = 0;
             if (t0 + lane < p.len) {
                 d = to_f<T>(dp[(p.row0 + (int64_t)(t0 + lane) * p.step) * a.lddt]) + bias;
                 if (a.softplus) d = softplus_f(d);
-                l = d * A2;
-                if (l < -150.0f) l = -150.0f;
+                gt = decay_of(d, A2);
             }
-            double gt = l;
-#pragma unroll
-            for (int m = 1; m < 32; m <<= 1) {
-                const double o = __shfl_up_sync(0xffffffffu, gt, m);
-                if (lane >= m) gt += o;
-            }
-            const double total = __shfl_sync(0xffffffffu, gt, 31);
+            gt = warp_scan(gt);
+            const long long total = __shfl_sync(0xffffffffu, gt, 31);
             s.g[lane] = gt;
             s.d[lane] = d;
-            s.eg[lane] = exp2f((float)gt);
-            s.w[lane] = d * exp2f((float)(total - gt));
-            if (lane == 0) s.keep = exp2f((float)total);
+            s.eg[lane] = exp2f(decay_f(gt));
+            s.w[lane] = d * exp2f(decay_f(total - gt));
+            if (lane == 0) s.keep = exp2f(decay_f(total));
             gsum += total;
         }
         __syncthreads();
@@ -192,7 +184,7 @@ __global__ void __launch_bounds__(2 * DV, DV == 128 ? 2 : 4) ssm_tc_kernel(SsmAr
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int t = rb + gq + (e >> 1) * 8, u = cb + 2 * tq + (e & 1);
-                    s.M[t][u] = u <= t ? exp2f((float)(s.g[t] - s.g[u])) * s.d[u] * (acc[0][e] + acc[1][e]) : 0.0f;
+                    s.M[t][u] = u <= t ? exp2f(decay_f(s.g[t] - s.g[u])) * s.d[u] * (acc[0][e] + acc[1][e]) : 0.0f;
                 }
             }
         }
@@ -310,7 +302,7 @@ __global__ void __launch_bounds__(2 * DV, DV == 128 ? 2 : 4) ssm_tc_kernel(SsmAr
 #pragma unroll
             for (int e = 0; e < 4; ++e) so[(8 * i + 2 * tq + (e & 1)) * DV + (e >> 1) * 8] = S[i][e];
     }
-    if (!FULL && tid == 0) ssm_decays(a, seg)[p.id * a.H + h] = exp2f((float)gsum);
+    if (!FULL && tid == 0) ssm_decays(a, seg)[p.id * a.H + h] = exp2f(decay_f(gsum));
 }
 
 template <typename T, int DK, int DV>

@@ -42,6 +42,7 @@
 namespace lq {
 namespace {
 
+constexpr int kSms = 148;
 constexpr int Q = 128;                 // tokens per chunk
 constexpr int PW = 64;                 // value columns of a group
 constexpr int HW = PW / 2;             // and of a thread
@@ -113,17 +114,6 @@ __device__ __forceinline__ uint32_t take_part(float2 &v) {
     return w;
 }
 
-__device__ __forceinline__ void tma_store_rows(const CUtensorMap *map, const void *src, int col, int b, int t) {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(col), "r"(b), "r"(t), "r"(smem_u32(src))
-                 : "memory");
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-// The stores have read their shared memory (done: and written theirs).
-__device__ __forceinline__ void tma_store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void tma_store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-
 // Rows t0 .. t0 + Q - 1 of a sequence (zeros from its end on), NCH chunks of 8
 // elements each, element by element: thread i of the group.
 __device__ __forceinline__ void copy_tile(unsigned char *dst, int nch, const bf16 *src, int64_t ld, const Piece &p,
@@ -140,25 +130,45 @@ __device__ __forceinline__ void copy_tile(unsigned char *dst, int nch, const bf1
     }
 }
 
-// Token rows [T][B][width] of x, B, C and y as 3-D maps, boxes of 64 columns x 128
+// Token rows [T][B][width] of x, B and C as 3-D maps, boxes of 64 columns x 128
 // tokens of one sequence (packed: one sequence of all rows).
 struct alignas(64) SsmMaps {
-    CUtensorMap x, b, c, y;
+    CUtensorMap x, b, c;
+};
+
+// One group's work: 64 value columns of one head over one piece.
+struct Item {
+    Piece p;
+    int h, c0, g;
+    int t_first, t_end;
+    int tm_t, tm_b;      // where TMA finds token t: row tm_t + t of sequence tm_b
+    bool valid;
+};
+
+// A group's share of the items: it takes every item that starts in its equal
+// part of all chunks, the items in the order of sequences, pieces and units.
+struct Walk {
+    int64_t pos, end;    // start of the next item and end of the share, in chunks
+    int b, j, u;         // the next item
 };
 
 struct Fixed {
-    uint64_t bar[4];     // G and C S done, Y done, B^T X' done, tiles arrived
-    double wsum[4];      // each warp's log2 decay
+    uint64_t bar[5];     // G and C S done, Y done, B^T X' done, B and C arrived, X arrived
+    long long wsum[2][4];   // each warp's log2 decay (even, odd chunks)
     int bad;             // a wait ran out
     int nf[2];           // a non-finite x in this chunk (even, odd chunks)
+    Item item[2];        // the item at work and the next
+    Walk walk;
     int first[2][PW];    // per value column, the first token whose x is not finite
 };
 
 // FULL: outputs and the final state; else only the pieces' own states (from
-// zero) and decays, for all but the last piece of each sequence.
+// zero) and decays, for all but the last piece of each sequence.  Each group
+// walks its share of the items; its second warp finds the next one and sends
+// for its first tiles before the last one ends.
 template <bool FULL, int DK>
 __global__ void __launch_bounds__(2 * kNT, 1)
-    ssm_umma_kernel(SsmArgs a, const __grid_constant__ SsmMaps maps, int seg, int units, int tma, int split) {
+    ssm_umma_kernel(SsmArgs a, const __grid_constant__ SsmMaps maps, int seg, int items, int tma, int split) {
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ uint32_t tmem;
     const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -166,89 +176,237 @@ __global__ void __launch_bounds__(2 * kNT, 1)
     unsigned char *sm = smem + grp * kSmem;
     Fixed &fx = reinterpret_cast<Fixed *>(smem + 2 * kSmem)[grp];
     const int warp = wid & 3, half = (wid >> 2) & 1, r = warp * 32 + lane;   // 32 rows, 32 columns of this warp
-    const int pairs = (units + 1) / 2;
-    const int z = blockIdx.x / pairs, u = 2 * (blockIdx.x % pairs) + grp;
-    Piece p;
-    if (!(FULL ? find_piece(a.r, seg, z, p) : find_cut(a.r, seg, z, p))) return;
-    const bool idle = u >= units;   // the second group of an odd number of units
+    // One thread of three warps issues for the group, so that none is held up for
+    // long: C B^T, C S and B^T X'; M X and the copies of X; the copies of B and C.
+    const bool lead = ti == 0, lead_x = ti == 128, finder = warp == 1 && half == 0;
+    const int units = a.H * (a.dv / PW);
+    const int64_t sall = (int64_t)a.H * DK * a.dv;
     auto sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(kNT) : "memory"); };
-    const int per = a.dv / PW;
-    const int h = idle ? 0 : u / per, c0 = (u % per) * PW;
-    const int g = (int)((int64_t)h * a.G / a.H);
-    const int t_first = p.j * seg, t_end = idle ? t_first : min(p.len, t_first + seg);
-    // where TMA finds token t: (row of its sequence, sequence)
-    const int tm_t = a.r.cu ? (int)p.row0 : 0, tm_b = a.r.cu ? 0 : p.b;
-    const bool lead = ti == 0;   // issues the group's copies and MMAs
 
-    // B and C of a chunk (their places are free once B^T X' of the chunk before
-    // is done), then X (free once its outputs are on their way).
-    auto load_bc = [&](int t0) {
-        mbar_arrive_expect_tx(&fx.bar[3], (FULL ? 2 : 1) * (DK / 64) * kBlk + kBlk);
-#pragma unroll
-        for (int j = 0; j < DK / 64; ++j) {
-            tma_rows(sm + kOffB + j * kBlk, &maps.b, g * DK + 64 * j, tm_b, tm_t + t0, &fx.bar[3]);
-            if (FULL) tma_rows(sm + kOffC + j * kBlk, &maps.c, g * DK + 64 * j, tm_b, tm_t + t0, &fx.bar[3]);
-        }
-    };
-    auto load_x = [&](int t0) { tma_rows(sm + kOffX, &maps.x, h * a.dv + c0, tm_b, tm_t + t0, &fx.bar[3]); };
-
-    if (lead) {
-        for (int i = 0; i < 4; ++i) mbar_init(&fx.bar[i], 1);
-        fx.bad = 0;
-        fence_mbar_init();
-        if (tma && t_first < t_end) {
-            load_bc(t_first);
-            load_x(t_first);
-        }
-    }
-    if (wid == 1) tmem_alloc(&tmem, 2 * kTmemCols);
-    {
-        const bf16 *xp = static_cast<const bf16 *>(a.x) + (int64_t)h * a.dv + c0;
-        const bf16 *dp = static_cast<const bf16 *>(a.dt) + h;
-        const float A2 = a.A[h] * 1.4426950408889634f;   // log2 decay per unit step
-        const float Dh = a.D ? a.D[h] : 0.0f, bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
-        if (DK < 128) {   // B^T has 128 rows: the missing key rows are zero
-            for (int i = ti; i < kBlk / 16; i += kNT)
-                reinterpret_cast<uint4 *>(sm + kOffB + kBlk)[i] = make_uint4(0u, 0u, 0u, 0u);
-        }
-        // A token's step and log2 decay, floored at -150 (a factor FP32 flushes to
-        // 0) so that no difference of sums is inf - inf; a NaN passes the comparison by.
-        auto raw_step = [&](int t) {
-            return t < p.len ? __bfloat162float(dp[(p.row0 + (int64_t)t * p.step) * a.lddt]) : 0.0f;
-        };
-        float d;
-        double gw;   // log2 decay up to this token within its warp's 32
-        auto scan_steps = [&](float raw, int t) {
-            d = 0.0f;
-            float l = 0.0f;
-            if (t < p.len) {
-                d = raw + bias;
-                if (a.softplus) d = softplus_f(d);
-                l = d * A2;
-                if (l < -150.0f) l = -150.0f;
-            }
-            gw = l;
-#pragma unroll
-            for (int m = 1; m < 32; m <<= 1) {
-                const double o = __shfl_up_sync(0xffffffffu, gw, m);
-                if (lane >= m) gw += o;
-            }
-            if (half == 0 && lane == 31) fx.wsum[warp] = gw;
-        };
-
-        // The state's key row r, this thread's columns.
-        float S[HW];
-        const int64_t soff = ((int64_t)h * DK + r) * a.dv + c0 + half * HW, sall = (int64_t)a.H * DK * a.dv;
+    float S[HW];   // the state's key row r, this thread's columns
+    // The item's state from its start, and to its end.
+    auto state_at = [&](const Item &it) { return ((int64_t)it.h * DK + r) * a.dv + it.c0 + half * HW; };
+    auto load_state = [&](const Item &it) {
         const float *S0 = nullptr;
-        if (FULL && !idle && r < DK) {
-            if (split && p.n > 1) S0 = a.ws + p.id * sall + soff;
-            else if (a.S0) S0 = a.S0 + p.b * sall + soff;
+        if (FULL && r < DK) {
+            if (split && it.p.n > 1) S0 = a.ws + it.p.id * sall + state_at(it);
+            else if (a.S0) S0 = a.S0 + it.p.b * sall + state_at(it);
         }
 #pragma unroll
         for (int i = 0; i < HW / 4; ++i) {
             const float4 v = S0 ? reinterpret_cast<const float4 *>(S0)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
             S[4 * i] = v.x; S[4 * i + 1] = v.y; S[4 * i + 2] = v.z; S[4 * i + 3] = v.w;
         }
+    };
+    auto store_state = [&](const Item &it) {
+        if (r < DK && (!FULL || it.p.j == it.p.n - 1)) {
+            float *so = (FULL ? a.S_out + it.p.b * sall : a.ws + it.p.id * sall) + state_at(it);
+#pragma unroll
+            for (int i = 0; i < HW / 4; ++i)
+                reinterpret_cast<float4 *>(so)[i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+        }
+    };
+    const int64_t worker = 2 * (int64_t)blockIdx.x + grp, workers = 2 * (int64_t)gridDim.x;
+    auto seq_len = [&](int b) {
+        return a.r.cu ? max(cu_at(a.r, b + 1) - cu_at(a.r, b), 0) : a.r.rows / a.r.B;
+    };
+    // (Both by the group's second warp.)  The first item that starts in this
+    // group's part; FULL only: the cut pieces are equal and dealt out in turn.
+    auto start_walk = [&]() {
+        Walk w{};
+        if (!FULL) {
+            w.pos = worker;
+            w.end = items;
+        } else {
+            int64_t all = 0;
+            for (int b = lane; b < a.r.B; b += 32) all += (seq_len(b) + Q - 1) / Q;
+            all = warp_scan(all);
+            all = __shfl_sync(0xffffffffu, all, 31) * units;
+            w.pos = all * worker / workers;
+            w.end = all * (worker + 1) / workers;
+            int64_t before = 0;   // chunks of the sequences before b
+            w.b = a.r.B;
+            for (int b0 = 0; b0 < a.r.B; b0 += 32) {
+                const int64_t n = b0 + lane < a.r.B ? (int64_t)((seq_len(b0 + lane) + Q - 1) / Q) * units : 0;
+                const int64_t upto = before + warp_scan(n);
+                const unsigned in = __ballot_sync(0xffffffffu, upto > w.pos);
+                if (in) {   // the sequence that holds the first position
+                    const int l = __ffs(in) - 1;
+                    w.b = b0 + l;
+                    before = __shfl_sync(0xffffffffu, upto - n, l);
+                    break;
+                }
+                before = __shfl_sync(0xffffffffu, upto, 31);
+            }
+            if (w.b < a.r.B) {
+                const int len = seq_len(w.b), n = (len + seg - 1) / seg, whole = seg / Q;
+                const int64_t o = w.pos - before, per = (int64_t)whole * units;
+                w.j = (int)min(o / per, (int64_t)(n - 1));
+                const int c = w.j < n - 1 ? whole : ((len - w.j * seg) + Q - 1) / Q;
+                w.u = (int)((o - w.j * per + c - 1) / c);
+                w.pos = before + w.j * per + (int64_t)w.u * c;
+            }
+        }
+        if (lane == 0) fx.walk = w;
+        __syncwarp();
+    };
+    auto next_item = [&](Item &out) {
+        Walk w = fx.walk;
+        Item it;
+        it.valid = false;
+        int u = 0;
+        if (!FULL) {
+            for (; w.pos < w.end && !it.valid; w.pos += workers) {
+                const int z = (int)(w.pos / units);
+                u = (int)(w.pos - (int64_t)z * units);
+                it.valid = find_cut(a.r, seg, z, it.p);
+            }
+        } else {
+            while (w.pos < w.end && w.b < a.r.B && !it.valid) {
+                const int c0 = a.r.cu ? cu_at(a.r, w.b) : 0, len = seq_len(w.b), n = (len + seg - 1) / seg;
+                if (w.u >= units) {
+                    w.u = 0;
+                    ++w.j;
+                }
+                if (w.j >= n) {
+                    w.j = w.u = 0;
+                    ++w.b;
+                    continue;
+                }
+                it.valid = true;
+                it.p.b = w.b;
+                it.p.j = w.j;
+                it.p.len = len;
+                it.p.n = n;
+                it.p.row0 = a.r.cu ? c0 : w.b;
+                it.p.step = a.r.cu ? 1 : a.r.B;
+                it.p.id = (a.r.cu ? c0 / seg + w.b : (int64_t)w.b * n) + w.j;
+                u = w.u++;
+                w.pos += (min(len - w.j * seg, seg) + Q - 1) / Q;
+            }
+        }
+        if (it.valid) {
+            const int per = a.dv / PW;
+            it.h = u / per;
+            it.c0 = (u % per) * PW;
+            it.g = (int)((int64_t)it.h * a.G / a.H);
+            it.t_first = it.p.j * seg;
+            it.t_end = min(it.p.len, it.t_first + seg);
+            it.tm_t = a.r.cu ? (int)it.p.row0 : 0;
+            it.tm_b = a.r.cu ? 0 : it.p.b;
+        }
+        __syncwarp();
+        if (lane == 0) {
+            out = it;
+            fx.walk = w;
+        }
+        __syncwarp();
+    };
+    // B and C of a chunk: their places are free once B^T X' of the chunk before is
+    // done.  X: once the outputs of the chunk before, in its place, have been stored.
+    auto load_bc = [&](const Item &it, int t0) {
+        mbar_arrive_expect_tx(&fx.bar[3], (FULL ? 2 : 1) * (DK / 64) * kBlk);
+#pragma unroll
+        for (int j = 0; j < DK / 64; ++j) {
+            tma_rows(sm + kOffB + j * kBlk, &maps.b, it.g * DK + 64 * j, it.tm_b, it.tm_t + t0, &fx.bar[3]);
+            if (FULL) tma_rows(sm + kOffC + j * kBlk, &maps.c, it.g * DK + 64 * j, it.tm_b, it.tm_t + t0, &fx.bar[3]);
+        }
+    };
+    auto load_x = [&](const Item &it, int t0) {
+        mbar_arrive_expect_tx(&fx.bar[4], kBlk);
+        tma_rows(sm + kOffX, &maps.x, it.h * a.dv + it.c0, it.tm_b, it.tm_t + t0, &fx.bar[4]);
+    };
+
+    if (finder) {
+        start_walk();
+        next_item(fx.item[0]);
+        if (lane == 0) {
+            for (int i = 0; i < 5; ++i) mbar_init(&fx.bar[i], 1);
+            fx.bad = 0;
+            fence_mbar_init();
+            if (tma && fx.item[0].valid) load_bc(fx.item[0], fx.item[0].t_first);
+        }
+    }
+    if (FULL && a.r.cu) {   // a sequence without tokens hands its state through
+        for (int b = blockIdx.x; b < a.r.B; b += gridDim.x)
+            if (cu_at(a.r, b + 1) <= cu_at(a.r, b))
+                for (int64_t i = threadIdx.x; i < sall / 4; i += 2 * kNT)
+                    reinterpret_cast<float4 *>(a.S_out + b * sall)[i] =
+                        a.S0 ? reinterpret_cast<const float4 *>(a.S0 + b * sall)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (wid == 1) tmem_alloc(&tmem, 2 * kTmemCols);
+    if (ti < 2 * PW) (&fx.first[0][0])[ti] = Q;
+    if (ti < 2) fx.nf[ti] = 0;
+    if (DK < 128) {   // B^T has 128 rows: the missing key rows are zero
+        for (int i = ti; i < kBlk / 16; i += kNT)
+            reinterpret_cast<uint4 *>(sm + kOffB + kBlk)[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = tmem + grp * kTmemCols, tl = tm + ((uint32_t)warp << 21);   // this warp's lanes: 32 warp
+
+    // This token's step and its log2 decay within its warp's 32, of the chunk
+    // after the one at work; and of the chunk at work: the step, 2^ of the decay
+    // within the warp and within the chunk, the weight in the next state, the
+    // factors for the rows of later warps.
+    float d_next, d, gwf, et, wr, keep, fac[3];
+    long long gw_next;
+    int parity = 0;
+    // The second group starts half a chunk behind the first.
+    if (grp == 0 && !fx.item[0].valid) asm volatile("bar.arrive 5, %0;" ::"n"(2 * kNT) : "memory");
+    if (grp == 1) asm volatile("bar.sync 5, %0;" ::"n"(2 * kNT) : "memory");
+    bool first = grp == 0;
+
+    for (int sel = 0; fx.item[sel].valid; sel ^= 1) {
+        const Item &it = fx.item[sel];
+        const Piece &p = it.p;
+        const int h = it.h, t_end = it.t_end;
+        const bf16 *dp = static_cast<const bf16 *>(a.dt) + h;
+        const float A2 = a.A[h] * 1.4426950408889634f;   // log2 decay per unit step
+        const float Dh = a.D ? a.D[h] : 0.0f, bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
+        // (as it is stored: the conversion would wait for it)
+        auto raw_step = [&](int t) -> unsigned short {
+            return t < p.len ? reinterpret_cast<const unsigned short *>(dp)[(p.row0 + (int64_t)t * p.step) * a.lddt]
+                             : (unsigned short)0;
+        };
+        auto scan_steps = [&](unsigned short raw, int t, int odd) {
+            d_next = 0.0f;
+            gw_next = 0;
+            if (t < p.len) {
+                d_next = bf16_to_f(raw) + bias;
+                if (a.softplus) d_next = softplus_f(d_next);
+                gw_next = decay_of(d_next, A2);
+            }
+            gw_next = warp_scan(gw_next);
+            if (half == 0 && lane == 31) fx.wsum[odd][warp] = gw_next;
+        };
+        long long gsum = 0;   // log2 decay of the piece so far
+        // The scanned chunk's factors, once every warp's sum is known.
+        auto finish_steps = [&](int odd) {
+            d = d_next;
+            long long base = 0, total = 0;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const long long s = fx.wsum[odd][w];
+                if (w < warp) base += s;
+                total += s;
+            }
+            const long long gt = base + gw_next;
+            gwf = decay_f(gw_next);
+            et = ex2_f(decay_f(gt));
+            wr = d * exp2f(decay_f(total - gt));
+            keep = exp2f(decay_f(total));
+            gsum += total;
+            if (FULL && half == 1) {
+                long long end = 0;
+#pragma unroll
+                for (int w = 0; w < 3; ++w) {
+                    end += fx.wsum[odd][w];
+                    fac[w] = d * exp2f(decay_f(end - gt));
+                }
+            }
+        };
         auto split_state = [&]() {   // the state's two parts
             if (FULL && r < DK) {
 #pragma unroll
@@ -265,64 +423,35 @@ __global__ void __launch_bounds__(2 * kNT, 1)
                 }
             }
         };
-        if (t_first < t_end) {
-            if (ti < 2 * PW) (&fx.first[0][0])[ti] = Q;
-            if (ti < 2) fx.nf[ti] = 0;
-            scan_steps(raw_step(t_first + r), t_first + r);
-            split_state();
-        }
-        tc_fence_before();
-        __syncthreads();
-        tc_fence_after();
-        const uint32_t tm = tmem + grp * kTmemCols, tl = tm + ((uint32_t)warp << 21);   // this warp's lanes: 32 warp
-        int parity = 0;
-        // the second group half a chunk behind the first
-        if (grp == 1 && t_first < t_end) asm volatile("bar.sync 5, %0;" ::"n"(2 * kNT) : "memory");
-        // A chunk's outputs, which are in X's place.
-        auto tma_store = [&](int t0) {
-            if (FULL) {
-                tma_store_rows(&maps.y, sm + kOffX, h * a.dv + c0, tm_b, tm_t + t0);
-                tma_store_read();
-            }
-        };
-        double gsum = 0.0;   // log2 decay of the piece so far
-        for (int t0 = t_first; t0 < t_end; t0 += Q, parity ^= 1) {
+        const unsigned short raw0 = raw_step(it.t_first + r), raw1 = raw_step(it.t_first + Q + r);
+        load_state(it);
+        scan_steps(raw0, it.t_first + r, 0);
+        split_state();
+        sync();
+        finish_steps(0);
+        scan_steps(raw1, it.t_first + Q + r, 1);
+        for (int t0 = it.t_first; t0 < t_end; t0 += Q, parity ^= 1) {
+            const bool tail = t0 + Q > p.len, last = t0 + Q >= t_end;
+            const int odd = ((t0 - it.t_first) / Q) & 1;
             fence_async_smem();
             tc_fence_before();
             sync();   // the chunk before is done with shared and tensor memory
-            if (lead && tma && t0 != t_first) {   // its outputs leave, the next X comes
-                tma_store(t0 - Q);
-                load_x(t0);
-            }
+            if (lead_x && tma) load_x(it, t0);
             if (fx.bad) {
-                if (lead && tma) mbar_wait_bounded(&fx.bar[3], parity, nullptr);   // the copies under way
+                if (lead_x && tma) {   // the copies under way
+                    mbar_wait_bounded(&fx.bar[3], parity, nullptr);
+                    mbar_wait_bounded(&fx.bar[4], parity, nullptr);
+                }
                 break;
             }
-            const float raw = raw_step(t0 + Q + r);   // the next chunk's step
-            if (ti < PW) fx.first[parity ^ 1][ti] = Q;
-            if (ti == 0) fx.nf[parity ^ 1] = 0;
-            double base = 0.0, total = 0.0;   // before this warp's tokens, and of the chunk
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                if (w < warp) base += fx.wsum[w];
-                total += fx.wsum[w];
-            }
-            const double gt = base + gw;
-            const float wr = d * exp2f((float)(total - gt));   // weight of this token in the next state
-            float fac[3];   // 2^(sum to the end of tokens 32 w .. - g_s) d_s for the rows of later warps
-            if (FULL && half == 1) {
-                double end = 0.0;
-#pragma unroll
-                for (int w = 0; w < 3; ++w) {
-                    end += fx.wsum[w];
-                    fac[w] = d * exp2f((float)(end - gt));
-                }
-            }
             if (tma) {
-                if (!mbar_wait_bounded(&fx.bar[3], parity, nullptr)) fx.bad = 1;
+                if (tail || lead) {
+                    if (!mbar_wait_bounded(&fx.bar[3], parity, nullptr)) fx.bad = 1;
+                }
                 __syncwarp();
-                if (t0 + Q > p.len) {
+                if (tail) {
                     // a packed sequence's last tile continues into the next sequence
+                    if (!mbar_wait_bounded(&fx.bar[4], parity, nullptr)) fx.bad = 1;
                     if (t0 + r >= p.len) {
                         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
@@ -337,9 +466,10 @@ __global__ void __launch_bounds__(2 * kNT, 1)
                     sync();
                 }
             } else {
-                copy_tile(sm + kOffB, DK / 8, static_cast<const bf16 *>(a.Bm) + g * DK, a.ldb, p, t0, ti);
-                copy_tile(sm + kOffX, PW / 8, xp, a.ldx, p, t0, ti);
-                if (FULL) copy_tile(sm + kOffC, DK / 8, static_cast<const bf16 *>(a.Cm) + g * DK, a.ldc, p, t0, ti);
+                copy_tile(sm + kOffB, DK / 8, static_cast<const bf16 *>(a.Bm) + it.g * DK, a.ldb, p, t0, ti);
+                copy_tile(sm + kOffX, PW / 8, static_cast<const bf16 *>(a.x) + (int64_t)h * a.dv + it.c0, a.ldx, p, t0,
+                          ti);
+                if (FULL) copy_tile(sm + kOffC, DK / 8, static_cast<const bf16 *>(a.Cm) + it.g * DK, a.ldc, p, t0, ti);
                 fence_async_smem();
                 sync();
             }
@@ -354,13 +484,18 @@ __global__ void __launch_bounds__(2 * kNT, 1)
                     mma_ss(tm + kColY, cd + step_k(k), sd + step_mn(k), idesc(2 * PW, 0, 1), k > 0);
                 umma_commit(&fx.bar[0]);
             }
+            __syncwarp();
+            const unsigned short raw = raw_step(t0 + 2 * Q + r);
+            if (ti < PW) fx.first[parity ^ 1][ti] = Q;
+            if (ti == 0) fx.nf[parity ^ 1] = 0;
+            if (tma && !mbar_wait_bounded(&fx.bar[4], parity, nullptr)) fx.bad = 1;
             if (FULL && !mbar_wait_bounded(&fx.bar[0], parity, nullptr)) fx.bad = 1;
             __syncwarp();
             tc_fence_after();
             float *fl = reinterpret_cast<float *>(sm + kOffF);   // [Q] sums within the warp, [Q] d, [3][Q] factors
             if (FULL) {
                 if (half == 0) {
-                    fl[r] = (float)gw;
+                    fl[r] = gwf;
                     fl[Q + r] = d;
                 } else {
 #pragma unroll
@@ -409,35 +544,36 @@ __global__ void __launch_bounds__(2 * kNT, 1)
             }
             __syncwarp();
             if (FULL) {
-                const float et = ex2_f((float)gt);   // 2^(g_t), on the sum of C S's parts
-                {
-                    uint32_t v[HW], v2[HW];
-                    tmem_ld_32x32b<HW>(tl + kColY + half * HW, v);
-                    tmem_ld_32x32b<HW>(tl + kColS + half * HW, v2);
+                // 2^(g_t) on the sum of C S's parts
+#pragma unroll 1
+                for (int q = 0; q < HW; q += 16) {
+                    uint32_t v[16], v2[16];
+                    tmem_ld_32x32b<16>(tl + kColY + half * HW + q, v);
+                    tmem_ld_32x32b<16>(tl + kColS + half * HW + q, v2);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < HW; ++i)
+                    for (int i = 0; i < 16; ++i)
                         v[i] = __float_as_uint(et * (__uint_as_float(v[i]) + __uint_as_float(v2[i])));
-                    tmem_st_32x32b_x32(tl + kColY + half * HW, v);
+                    tmem_st_32x32b_x16(tl + kColY + half * HW + q, v);
                 }
                 sync();   // the factors
-                // M over G, 32 columns at a time: 16 columns of first parts, 16 of
-                // second.  Columns of earlier warps' tokens factor through the
-                // boundary before this warp's, later ones are zero.
-                const float gwf = (float)gw, rf = ex2_f(gwf);
-                for (int q = half; q < 4; q += 2) {
-                    uint32_t v[32];
-                    if (q > warp) {
+                // M over G, 16 tokens at a time: 8 columns of first parts, 8 of
+                // second.  Tokens of earlier warps factor through the boundary
+                // before this warp's, those after this one are zero.
+                const float rf = ex2_f(gwf);
+                for (int q = half; q < 8; q += 2) {
+                    uint32_t v[16];
+                    if (q > 2 * warp + 1) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = 0u;
+                        for (int i = 0; i < 16; ++i) v[i] = 0u;
                     } else {
-                        tmem_ld_32x32b<32>(tl + 32 * q, v);
+                        tmem_ld_32x32b<16>(tl + 16 * q, v);
                         tmem_ld_wait();
-                        uint32_t hi[16], lo[16];
-                        if (q < warp) {
-                            const float4 *cf = reinterpret_cast<const float4 *>(fl + (1 + warp) * Q + 32 * q);
+                        uint32_t hi[8], lo[8];
+                        if (q < 2 * warp) {
+                            const float4 *cf = reinterpret_cast<const float4 *>(fl + (1 + warp) * Q + 16 * q);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
+                            for (int i = 0; i < 4; ++i) {
                                 const float4 c = cf[i];
                                 const float2 cc[2] = {f2(c.x, c.y), f2(c.z, c.w)};
 #pragma unroll
@@ -450,17 +586,17 @@ __global__ void __launch_bounds__(2 * kNT, 1)
                                 }
                             }
                         } else {
-                            const float4 *gs = reinterpret_cast<const float4 *>(fl + 32 * q);
-                            const float4 *ds = reinterpret_cast<const float4 *>(fl + Q + 32 * q);
+                            const float4 *gs = reinterpret_cast<const float4 *>(fl + 16 * q);
+                            const float4 *ds = reinterpret_cast<const float4 *>(fl + Q + 16 * q);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
+                            for (int i = 0; i < 4; ++i) {
                                 const float4 gv = gs[i], dv = ds[i];
                                 const float ge[4] = {gv.x, gv.y, gv.z, gv.w}, de[4] = {dv.x, dv.y, dv.z, dv.w};
                                 float m[4];
 #pragma unroll
                                 for (int k = 0; k < 4; ++k) {
                                     const float e = ex2_f(gwf - ge[k]) * de[k] * __uint_as_float(v[4 * i + k]);
-                                    m[k] = 4 * i + k <= lane ? e : 0.0f;
+                                    m[k] = 16 * (q & 1) + 4 * i + k <= lane ? e : 0.0f;
                                 }
 #pragma unroll
                                 for (int k = 0; k < 2; ++k) {
@@ -471,21 +607,29 @@ __global__ void __launch_bounds__(2 * kNT, 1)
                             }
                         }
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
+                        for (int i = 0; i < 8; ++i) {
                             v[i] = hi[i];
-                            v[16 + i] = lo[i];
+                            v[8 + i] = lo[i];
                         }
                     }
-                    tmem_st_32x32b_x32(tl + 32 * q, v);
+                    tmem_st_32x32b_x16(tl + 16 * q, v);
                 }
                 tmem_st_wait();
+            }
+            // The next chunk's factors and the decays of the one after: by the
+            // issuing warp (which has little of M) before it is held up, by the
+            // others while the MMAs run.
+            const float keep_now = keep;
+            if (FULL && !last && warp == 0) {
+                finish_steps(odd ^ 1);
+                scan_steps(raw, t0 + 2 * Q + r, odd);
             }
             fence_async_smem();
             tc_fence_before();
             sync();
             if (lead) {
                 tc_fence_after();
-                const uint64_t bd = desc_mn(sm + kOffB), wd = desc_mn(sm + kOffXw), xd = desc_mn(sm + kOffX);
+                const uint64_t bd = desc_mn(sm + kOffB), wd = desc_mn(sm + kOffXw);
 #pragma unroll
                 for (int part = 0; part < 3; ++part)
 #pragma unroll
@@ -493,72 +637,86 @@ __global__ void __launch_bounds__(2 * kNT, 1)
                         mma_ss(tm + kColS, bd + step_mn(k), wd + (part * kBlk >> 4) + step_mn(k), idesc(PW, 1, 1),
                                part + k > 0);
                 umma_commit(&fx.bar[2]);
-                if (FULL) {
+            }
+            if (FULL && lead_x) {
+                tc_fence_after();
+                const uint64_t xd = desc_mn(sm + kOffX);
+                {
 #pragma unroll
                     for (int k = 0; k < Q / 16; ++k)
 #pragma unroll
                         for (int part = 0; part < 2; ++part)
-                            mma_ts(tm + kColY, tm + 32 * (k >> 1) + 16 * part + 8 * (k & 1), xd + step_mn(k),
+                            mma_ts(tm + kColY, tm + 16 * k + 8 * part, xd + step_mn(k),
                                    idesc(PW, 0, 1), 1);
                     umma_commit(&fx.bar[1]);
                 }
             }
             __syncwarp();
-            if (t0 == t_first && grp == 0 && u + 1 < units)
-                asm volatile("bar.arrive 5, %0;" ::"n"(2 * kNT) : "memory");
-            const float keep = exp2f((float)total);
-            gsum += total;
-            if (t0 + Q < t_end) scan_steps(raw, t0 + Q + r);
+            if (first) asm volatile("bar.arrive 5, %0;" ::"n"(2 * kNT) : "memory");
+            first = false;
+            if (!last && (!FULL || warp != 0)) {
+                finish_steps(odd ^ 1);
+                scan_steps(raw, t0 + 2 * Q + r, odd);
+            }
+            if (last && finder) next_item(fx.item[sel ^ 1]);
             if (!mbar_wait_bounded(&fx.bar[2], parity, nullptr)) fx.bad = 1;
-            if (lead && tma && t0 + Q < t_end) load_bc(t0 + Q);
+            if (finder && lane == 0 && tma) {
+                if (!last) load_bc(it, t0 + Q);
+                else if (fx.item[sel ^ 1].valid) load_bc(fx.item[sel ^ 1], fx.item[sel ^ 1].t_first);
+            }
             __syncwarp();
             tc_fence_after();
-            {
-                uint32_t v[HW];
-                tmem_ld_32x32b<HW>(tl + kColS + half * HW, v);
+#pragma unroll
+            for (int q = 0; q < HW; q += 16) {
+                uint32_t v[16];
+                tmem_ld_32x32b<16>(tl + kColS + half * HW + q, v);
                 tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < HW; i += 2) {
-                    const float2 s = ffma2(f2(keep, keep), f2(S[i], S[i + 1]),
+                for (int i = 0; i < 16; i += 2) {
+                    const float2 s = ffma2(f2(keep_now, keep_now), f2(S[q + i], S[q + i + 1]),
                                            f2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
-                    S[i] = s.x;
-                    S[i + 1] = s.y;
+                    S[q + i] = s.x;
+                    S[q + i + 1] = s.y;
                 }
             }
-            split_state();
+            if (!last) split_state();
             if (FULL) {
-                // outputs into X's place; full tiles leave by a tensor store
+                // outputs into X's place
                 if (!mbar_wait_bounded(&fx.bar[1], parity, nullptr)) fx.bad = 1;
                 __syncwarp();
                 tc_fence_after();
                 const bool nf = fx.nf[parity] != 0;
-                uint32_t v[HW];
-                tmem_ld_32x32b<HW>(tl + kColY + half * HW, v);
-                tmem_ld_wait();
+#pragma unroll 1
+                for (int q = 0; q < HW; q += 16) {
+                    uint32_t v[16];
+                    tmem_ld_32x32b<16>(tl + kColY + half * HW + q, v);
+                    tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < HW / 8; ++j) {
-                    uint4 *at = chunk(sm + kOffX, r, half * (HW / 8) + j);
-                    Raw<bf16, 8> rx;
-                    rx.a = *at;
-                    float f[8];
-                    rx.get(f);
+                    for (int j = 0; j < 2; ++j) {
+                        uint4 *at8 = chunk(sm + kOffX, r, half * (HW / 8) + q / 8 + j);
+                        Raw<bf16, 8> rx;
+                        rx.a = *at8;
+                        float f[8];
+                        rx.get(f);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) f[k] = fmaf(Dh, f[k], __uint_as_float(v[8 * j + k]));
-                    if (nf)
+                        for (int k = 0; k < 8; ++k) f[k] = fmaf(Dh, f[k], __uint_as_float(v[8 * j + k]));
+                        if (nf)
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            if (fx.first[parity][half * HW + 8 * j + k] <= r) f[k] = __int_as_float(0x7fffffff);
-                    rx.set(f);
-                    *at = rx.a;
+                            for (int k = 0; k < 8; ++k)
+                                if (fx.first[parity][half * HW + q + 8 * j + k] <= r) f[k] = __int_as_float(0x7fffffff);
+                        rx.set(f);
+                        *at8 = rx.a;
+                    }
                 }
-                if (!tma || t0 + Q > p.len) {   // element by element: unaligned rows, a sequence's last rows
-                    sync();
-                    for (int i = ti; i < Q * (PW / 8); i += kNT) {
-                        const int t = i / (PW / 8), j = i % (PW / 8);
-                        if (t0 + t >= p.len) break;
+                // whole rows of 128 bytes at a time
+                sync();
+                const int col = h * a.dv + it.c0;
+#pragma unroll
+                for (int i = 0; i < Q * (PW / 8) / kNT; ++i) {
+                    const int t = (i * kNT + ti) / (PW / 8), j = ti % (PW / 8);
+                    if (t0 + t < p.len) {
                         const uint4 w4 = *chunk(sm + kOffX, t, j);
-                        bf16 *dst = static_cast<bf16 *>(a.y) + (p.row0 + (int64_t)(t0 + t) * p.step) * a.ldy +
-                                    (int64_t)h * a.dv + c0 + 8 * j;
+                        bf16 *dst = static_cast<bf16 *>(a.y) + (p.row0 + (int64_t)(t0 + t) * p.step) * a.ldy + col + 8 * j;
                         if (tma) {
                             *reinterpret_cast<uint4 *>(dst) = w4;
                         } else {
@@ -574,24 +732,14 @@ __global__ void __launch_bounds__(2 * kNT, 1)
                 }
             }
         }
-        fence_async_smem();
-        sync();
-        const int t_last = t_first + (t_end - t_first - 1) / Q * Q;   // the last chunk
-        if (FULL && lead && tma && t_first < t_end && t_last + Q <= p.len && !fx.bad) {
-            tma_store(t_last);
-            tma_store_done();
-        }
+        sync();   // the next item is known
         // A wait that ran out leaves no state that looks like one.
         if (fx.bad)
 #pragma unroll
             for (int i = 0; i < HW; ++i) S[i] = __int_as_float(0x7fffffff);
-        if (!idle && r < DK && (!FULL || p.j == p.n - 1)) {
-            float *so = FULL ? a.S_out + p.b * sall + soff : a.ws + p.id * sall + soff;
-#pragma unroll
-            for (int i = 0; i < HW / 4; ++i)
-                reinterpret_cast<float4 *>(so)[i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
-        }
-        if (!FULL && !idle && ti == 0 && c0 == 0) ssm_decays(a, seg)[p.id * a.H + h] = exp2f((float)gsum);
+        store_state(it);
+        if (fx.bad) break;
+        if (!FULL && ti == 0 && it.c0 == 0) ssm_decays(a, seg)[p.id * a.H + h] = exp2f(decay_f(gsum));
     }
     tc_fence_before();
     __syncthreads();
@@ -630,20 +778,20 @@ template <int DK>
 cudaError_t launch(const SsmArgs &a, const SsmMaps &maps, int seg, int tma, int split, cudaStream_t s) {
     constexpr int bytes = 2 * (kSmem + (int)sizeof(Fixed));
     static_assert(bytes <= 226 * 1024, "shared memory of one CTA");
-    const int units = a.H * (a.dv / PW);
-    const int64_t pairs = (units + 1) / 2;
+    const int64_t units = (int64_t)a.H * (a.dv / PW);
+    auto grid = [](int64_t items) { return (unsigned)(items < 2 * kSms ? (items + 1) / 2 : kSms); };
     cudaError_t e = cudaFuncSetAttribute(ssm_umma_kernel<true, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     if (split) {
         e = cudaFuncSetAttribute(ssm_umma_kernel<false, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
-        ssm_umma_kernel<false, DK><<<(unsigned)(cut_count(a.r, seg) * pairs), 2 * kNT, bytes, s>>>(a, maps, seg, units,
-                                                                                                tma, split);
+        const int64_t cuts = cut_count(a.r, seg) * units;
+        ssm_umma_kernel<false, DK><<<grid(cuts), 2 * kNT, bytes, s>>>(a, maps, seg, (int)cuts, tma, split);
         e = launch_ssm_join(a, seg, s);
         if (e != cudaSuccess) return e;
     }
-    ssm_umma_kernel<true, DK><<<(unsigned)(piece_count(a.r, seg) * pairs), 2 * kNT, bytes, s>>>(a, maps, seg, units,
-                                                                                              tma, split);
+    const int64_t items = piece_count(a.r, seg) * units;
+    ssm_umma_kernel<true, DK><<<grid(items), 2 * kNT, bytes, s>>>(a, maps, seg, (int)items, tma, split);
     return cudaGetLastError();
 }
 
@@ -657,8 +805,7 @@ cudaError_t launch_ssm_umma(const SsmArgs &a, int seg, bool split, cudaStream_t 
     const bool tma = base % 16 == 0 && a.ldx % 8 == 0 && a.ldb % 8 == 0 && a.ldc % 8 == 0 && a.ldy % 8 == 0 &&
                      encode(&maps.x, a.x, a.r, (int64_t)a.H * a.dv, a.ldx) &&
                      encode(&maps.b, a.Bm, a.r, (int64_t)a.G * a.dk, a.ldb) &&
-                     encode(&maps.c, a.Cm, a.r, (int64_t)a.G * a.dk, a.ldc) &&
-                     encode(&maps.y, a.y, a.r, (int64_t)a.H * a.dv, a.ldy);
+                     encode(&maps.c, a.Cm, a.r, (int64_t)a.G * a.dk, a.ldc);
     return a.dk == 64 ? launch<64>(a, maps, seg, tma, split, s) : launch<128>(a, maps, seg, tma, split, s);
 }
 
