@@ -121,37 +121,26 @@ cudaError_t launch_ssm_step(const SsmArgs &a, int dtype, cudaStream_t s) {
 
 namespace {
 
-// One thread per 4 state elements of one sequence and head.
-__global__ void __launch_bounds__(256) ssm_join_kernel(SsmArgs a, int seg) {
-    const int64_t per = (int64_t)a.dk * a.dv / 4;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;   // (head, element), same sequence for the CTA row
-    if (i >= per * a.H) return;
-    for (int b = blockIdx.y; b < a.r.B; b += gridDim.y) {
-        int64_t z0;
-        int n;
-        if (a.r.cu) {
-            const int c0 = cu_at(a.r, b), len = max(cu_at(a.r, b + 1), c0) - c0;
-            z0 = c0 / seg + b;
-            n = (len + seg - 1) / seg;
-        } else {
-            n = (a.r.rows / a.r.B + seg - 1) / seg;
-            z0 = (int64_t)b * n;
-        }
-        if (n < 2) continue;
-        const int h = (int)(i / per);
-        const float *decay = ssm_decays(a, seg) + z0 * a.H + h;
-        float4 *slot = reinterpret_cast<float4 *>(a.ws) + z0 * a.H * per + i;
-        float4 S = a.S0 ? reinterpret_cast<const float4 *>(a.S0)[(int64_t)b * a.H * per + i]
-                        : make_float4(0.f, 0.f, 0.f, 0.f);
+// One thread per 4 state elements of a sequence; blockIdx.y counts the places
+// where a sequence may be cut, its first one does the work.
+__global__ void __launch_bounds__(256) ssm_join_kernel(SsmArgs a, int seg, int cuts) {
+    const int64_t per = (int64_t)a.dk * a.dv / 4, all = per * a.H;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;   // (head, element)
+    for (int k = blockIdx.y; k < cuts; k += gridDim.y) {
+        Piece p;
+        if (!find_cut(a.r, seg, k, p) || p.j != 0 || i >= all) continue;
+        const float *decay = ssm_decays(a, seg) + p.id * a.H + i / per;
+        float4 *slot = reinterpret_cast<float4 *>(a.ws) + p.id * all + i;
+        float4 S = a.S0 ? reinterpret_cast<const float4 *>(a.S0)[p.b * all + i] : make_float4(0.f, 0.f, 0.f, 0.f);
         float4 own = slot[0];
-        for (int j = 0; j < n; ++j) {
-            float4 *at = slot + (int64_t)j * a.H * per;
+        for (int j = 0; j < p.n; ++j) {
+            float4 *at = slot + j * all;
             float4 next = own;
-            if (j + 2 < n) next = at[a.H * per];   // the last piece has no state of its own
+            if (j + 2 < p.n) next = at[all];   // the last piece has no state of its own
             *at = S;
-            if (j + 1 < n) {
-                const float k = decay[(int64_t)j * a.H];
-                S = make_float4(fmaf(k, S.x, own.x), fmaf(k, S.y, own.y), fmaf(k, S.z, own.z), fmaf(k, S.w, own.w));
+            if (j + 1 < p.n) {
+                const float f = decay[(int64_t)j * a.H];
+                S = make_float4(fmaf(f, S.x, own.x), fmaf(f, S.y, own.y), fmaf(f, S.z, own.z), fmaf(f, S.w, own.w));
             }
             own = next;
         }
@@ -177,8 +166,9 @@ bool may_split(const Rows &r, int seg) { return (r.cu ? r.rows : r.rows / r.B) >
 }  // namespace
 
 cudaError_t launch_ssm_join(const SsmArgs &a, int seg, cudaStream_t s) {
-    const int64_t n = (int64_t)a.H * a.dk * a.dv / 4;
-    ssm_join_kernel<<<dim3((unsigned)((n + 255) / 256), a.r.B < 65535 ? a.r.B : 65535), 256, 0, s>>>(a, seg);
+    const int64_t n = (int64_t)a.H * a.dk * a.dv / 4, cuts = cut_count(a.r, seg);
+    ssm_join_kernel<<<dim3((unsigned)((n + 255) / 256), (unsigned)(cuts < 65535 ? cuts : 65535)), 256, 0, s>>>(
+        a, seg, (int)cuts);
     return cudaGetLastError();
 }
 

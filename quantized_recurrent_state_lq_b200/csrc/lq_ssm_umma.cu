@@ -162,13 +162,34 @@ struct Fixed {
     int first[2][PW];    // per value column, the first token whose x is not finite
 };
 
-// FULL: outputs and the final state; else only the pieces' own states (from
-// zero) and decays, for all but the last piece of each sequence.  Each group
-// walks its share of the items; its second warp finds the next one and sends
-// for its first tiles before the last one ends.
-template <bool FULL, int DK>
+// X' of token r, this thread's columns, in three parts: w x.
+__device__ __forceinline__ void split_x(unsigned char *sm, unsigned char *x, int r, int half, float w) {
+#pragma unroll
+    for (int i = 0; i < HW / 8; ++i) {
+        const int j = half * (HW / 8) + i;
+        Raw<bf16, 8> rx;
+        rx.a = *chunk(x, r, j);
+        float f[8];
+        rx.get(f);
+        uint32_t part[3][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float2 v = mul2(f2(w, w), f2(f[2 * k], f[2 * k + 1]));
+            part[0][k] = take_part(v);
+            part[1][k] = take_part(v);
+            part[2][k] = last_part(v);
+        }
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+            *chunk(sm + kOffXw + q * kBlk, r, j) = make_uint4(part[q][0], part[q][1], part[q][2], part[q][3]);
+    }
+}
+
+// Outputs and final states.  Each group walks its share of the items; its second
+// warp finds the next one and sends for its first tiles before the last one ends.
+template <int DK>
 __global__ void __launch_bounds__(2 * kNT, 1)
-    ssm_umma_kernel(SsmArgs a, const __grid_constant__ SsmMaps maps, int seg, int items, int tma, int split) {
+    ssm_umma_kernel(SsmArgs a, const __grid_constant__ SsmMaps maps, int seg, int tma, int split) {
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ uint32_t tmem;
     const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -188,7 +209,7 @@ __global__ void __launch_bounds__(2 * kNT, 1)
     auto state_at = [&](const Item &it) { return ((int64_t)it.h * DK + r) * a.dv + it.c0 + half * HW; };
     auto load_state = [&](const Item &it) {
         const float *S0 = nullptr;
-        if (FULL && r < DK) {
+        if (r < DK) {
             if (split && it.p.n > 1) S0 = a.ws + it.p.id * sall + state_at(it);
             else if (a.S0) S0 = a.S0 + it.p.b * sall + state_at(it);
         }
@@ -199,8 +220,8 @@ __global__ void __launch_bounds__(2 * kNT, 1)
         }
     };
     auto store_state = [&](const Item &it) {
-        if (r < DK && (!FULL || it.p.j == it.p.n - 1)) {
-            float *so = (FULL ? a.S_out + it.p.b * sall : a.ws + it.p.id * sall) + state_at(it);
+        if (r < DK && it.p.j == it.p.n - 1) {
+            float *so = a.S_out + it.p.b * sall + state_at(it);
 #pragma unroll
             for (int i = 0; i < HW / 4; ++i)
                 reinterpret_cast<float4 *>(so)[i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
@@ -211,13 +232,10 @@ __global__ void __launch_bounds__(2 * kNT, 1)
         return a.r.cu ? max(cu_at(a.r, b + 1) - cu_at(a.r, b), 0) : a.r.rows / a.r.B;
     };
     // (Both by the group's second warp.)  The first item that starts in this
-    // group's part; FULL only: the cut pieces are equal and dealt out in turn.
+    // group's part.
     auto start_walk = [&]() {
         Walk w{};
-        if (!FULL) {
-            w.pos = worker;
-            w.end = items;
-        } else {
+        {
             int64_t all = 0;
             for (int b = lane; b < a.r.B; b += 32) all += (seq_len(b) + Q - 1) / Q;
             all = warp_scan(all);
@@ -255,13 +273,7 @@ __global__ void __launch_bounds__(2 * kNT, 1)
         Item it;
         it.valid = false;
         int u = 0;
-        if (!FULL) {
-            for (; w.pos < w.end && !it.valid; w.pos += workers) {
-                const int z = (int)(w.pos / units);
-                u = (int)(w.pos - (int64_t)z * units);
-                it.valid = find_cut(a.r, seg, z, it.p);
-            }
-        } else {
+        {
             while (w.pos < w.end && w.b < a.r.B && !it.valid) {
                 const int c0 = a.r.cu ? cu_at(a.r, w.b) : 0, len = seq_len(w.b), n = (len + seg - 1) / seg;
                 if (w.u >= units) {
@@ -305,11 +317,11 @@ __global__ void __launch_bounds__(2 * kNT, 1)
     // B and C of a chunk: their places are free once B^T X' of the chunk before is
     // done.  X: once the outputs of the chunk before, in its place, have been stored.
     auto load_bc = [&](const Item &it, int t0) {
-        mbar_arrive_expect_tx(&fx.bar[3], (FULL ? 2 : 1) * (DK / 64) * kBlk);
+        mbar_arrive_expect_tx(&fx.bar[3], 2 * (DK / 64) * kBlk);
 #pragma unroll
         for (int j = 0; j < DK / 64; ++j) {
             tma_rows(sm + kOffB + j * kBlk, &maps.b, it.g * DK + 64 * j, it.tm_b, it.tm_t + t0, &fx.bar[3]);
-            if (FULL) tma_rows(sm + kOffC + j * kBlk, &maps.c, it.g * DK + 64 * j, it.tm_b, it.tm_t + t0, &fx.bar[3]);
+            tma_rows(sm + kOffC + j * kBlk, &maps.c, it.g * DK + 64 * j, it.tm_b, it.tm_t + t0, &fx.bar[3]);
         }
     };
     auto load_x = [&](const Item &it, int t0) {
@@ -327,7 +339,7 @@ __global__ void __launch_bounds__(2 * kNT, 1)
             if (tma && fx.item[0].valid) load_bc(fx.item[0], fx.item[0].t_first);
         }
     }
-    if (FULL && a.r.cu) {   // a sequence without tokens hands its state through
+    if (a.r.cu) {   // a sequence without tokens hands its state through
         for (int b = blockIdx.x; b < a.r.B; b += gridDim.x)
             if (cu_at(a.r, b + 1) <= cu_at(a.r, b))
                 for (int64_t i = threadIdx.x; i < sall / 4; i += 2 * kNT)
@@ -381,7 +393,6 @@ __global__ void __launch_bounds__(2 * kNT, 1)
             gw_next = warp_scan(gw_next);
             if (half == 0 && lane == 31) fx.wsum[odd][warp] = gw_next;
         };
-        long long gsum = 0;   // log2 decay of the piece so far
         // The scanned chunk's factors, once every warp's sum is known.
         auto finish_steps = [&](int odd) {
             d = d_next;
@@ -397,8 +408,7 @@ __global__ void __launch_bounds__(2 * kNT, 1)
             et = ex2_f(decay_f(gt));
             wr = d * exp2f(decay_f(total - gt));
             keep = exp2f(decay_f(total));
-            gsum += total;
-            if (FULL && half == 1) {
+            if (half == 1) {
                 long long end = 0;
 #pragma unroll
                 for (int w = 0; w < 3; ++w) {
@@ -408,7 +418,7 @@ __global__ void __launch_bounds__(2 * kNT, 1)
             }
         };
         auto split_state = [&]() {   // the state's two parts
-            if (FULL && r < DK) {
+            if (r < DK) {
 #pragma unroll
                 for (int j = 0; j < HW / 8; ++j) {
                     uint32_t hi[4], lo[4];
@@ -457,7 +467,7 @@ __global__ void __launch_bounds__(2 * kNT, 1)
 #pragma unroll
                         for (int j = 0; j < DK / 16; ++j) {
                             *chunk(sm + kOffB, r, half * (DK / 16) + j) = zero;
-                            if (FULL) *chunk(sm + kOffC, r, half * (DK / 16) + j) = zero;
+                            *chunk(sm + kOffC, r, half * (DK / 16) + j) = zero;
                         }
 #pragma unroll
                         for (int j = 0; j < PW / 16; ++j) *chunk(sm + kOffX, r, half * (PW / 16) + j) = zero;
@@ -469,11 +479,11 @@ __global__ void __launch_bounds__(2 * kNT, 1)
                 copy_tile(sm + kOffB, DK / 8, static_cast<const bf16 *>(a.Bm) + it.g * DK, a.ldb, p, t0, ti);
                 copy_tile(sm + kOffX, PW / 8, static_cast<const bf16 *>(a.x) + (int64_t)h * a.dv + it.c0, a.ldx, p, t0,
                           ti);
-                if (FULL) copy_tile(sm + kOffC, DK / 8, static_cast<const bf16 *>(a.Cm) + it.g * DK, a.ldc, p, t0, ti);
+                copy_tile(sm + kOffC, DK / 8, static_cast<const bf16 *>(a.Cm) + it.g * DK, a.ldc, p, t0, ti);
                 fence_async_smem();
                 sync();
             }
-            if (FULL && lead) {
+            if (lead) {
                 tc_fence_after();
                 const uint64_t cd = desc_k(sm + kOffC), bd = desc_k(sm + kOffB), sd = desc_mn(sm + kOffS);
 #pragma unroll
@@ -489,11 +499,11 @@ __global__ void __launch_bounds__(2 * kNT, 1)
             if (ti < PW) fx.first[parity ^ 1][ti] = Q;
             if (ti == 0) fx.nf[parity ^ 1] = 0;
             if (tma && !mbar_wait_bounded(&fx.bar[4], parity, nullptr)) fx.bad = 1;
-            if (FULL && !mbar_wait_bounded(&fx.bar[0], parity, nullptr)) fx.bad = 1;
+            if (!mbar_wait_bounded(&fx.bar[0], parity, nullptr)) fx.bad = 1;
             __syncwarp();
             tc_fence_after();
             float *fl = reinterpret_cast<float *>(sm + kOffF);   // [Q] sums within the warp, [Q] d, [3][Q] factors
-            if (FULL) {
+            {
                 if (half == 0) {
                     fl[r] = gwf;
                     fl[Q + r] = d;
@@ -523,7 +533,7 @@ __global__ void __launch_bounds__(2 * kNT, 1)
 #pragma unroll
                 for (int q = 0; q < 3; ++q)
                     *chunk(sm + kOffXw + q * kBlk, r, j) = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
-                if (FULL) {
+                {
                     const uint32_t wd[4] = {rx.a.x, rx.a.y, rx.a.z, rx.a.w};
                     __nv_bfloat162 n = __float2bfloat162_rn(0.0f);   // 0 x finite = 0, else NaN
 #pragma unroll
@@ -543,7 +553,7 @@ __global__ void __launch_bounds__(2 * kNT, 1)
                 }
             }
             __syncwarp();
-            if (FULL) {
+            {
                 // 2^(g_t) on the sum of C S's parts
 #pragma unroll 1
                 for (int q = 0; q < HW; q += 16) {
@@ -620,7 +630,7 @@ __global__ void __launch_bounds__(2 * kNT, 1)
             // issuing warp (which has little of M) before it is held up, by the
             // others while the MMAs run.
             const float keep_now = keep;
-            if (FULL && !last && warp == 0) {
+            if (!last && warp == 0) {
                 finish_steps(odd ^ 1);
                 scan_steps(raw, t0 + 2 * Q + r, odd);
             }
@@ -638,7 +648,7 @@ __global__ void __launch_bounds__(2 * kNT, 1)
                                part + k > 0);
                 umma_commit(&fx.bar[2]);
             }
-            if (FULL && lead_x) {
+            if (lead_x) {
                 tc_fence_after();
                 const uint64_t xd = desc_mn(sm + kOffX);
                 {
@@ -654,7 +664,7 @@ __global__ void __launch_bounds__(2 * kNT, 1)
             __syncwarp();
             if (first) asm volatile("bar.arrive 5, %0;" ::"n"(2 * kNT) : "memory");
             first = false;
-            if (!last && (!FULL || warp != 0)) {
+            if (!last && warp != 0) {
                 finish_steps(odd ^ 1);
                 scan_steps(raw, t0 + 2 * Q + r, odd);
             }
@@ -680,7 +690,7 @@ __global__ void __launch_bounds__(2 * kNT, 1)
                 }
             }
             if (!last) split_state();
-            if (FULL) {
+            {
                 // outputs into X's place
                 if (!mbar_wait_bounded(&fx.bar[1], parity, nullptr)) fx.bad = 1;
                 __syncwarp();
@@ -739,13 +749,191 @@ __global__ void __launch_bounds__(2 * kNT, 1)
             for (int i = 0; i < HW; ++i) S[i] = __int_as_float(0x7fffffff);
         store_state(it);
         if (fx.bad) break;
-        if (!FULL && ti == 0 && it.c0 == 0) ssm_decays(a, seg)[p.id * a.H + h] = exp2f(decay_f(gsum));
     }
     tc_fence_before();
     __syncthreads();
     if (wid == 1) {
         tmem_relinquish();
         tmem_dealloc(tmem, 2 * kTmemCols);
+    }
+}
+
+// The pieces' own states, from zero, and their decays, for every piece that is
+// followed by another (all of them seg tokens long): only B^T X' and the state
+// update.  Without C and S the tiles of X have two places, a chunk ahead, and
+// the products of a chunk two accumulators, so that the update runs beside the
+// next chunk's MMAs.
+//   [0, 48K) X' parts, [48K, 64K) X of even chunks, [64K, 96K) B, [96K, 112K) X of odd chunks
+template <int DK>
+__global__ void __launch_bounds__(2 * kNT, 1)
+    ssm_state_kernel(SsmArgs a, const __grid_constant__ SsmMaps maps, int seg, int64_t items, int tma) {
+    extern __shared__ __align__(1024) unsigned char smem[];
+    __shared__ uint32_t tmem;
+    const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int grp = threadIdx.x / kNT, ti = threadIdx.x % kNT;
+    unsigned char *sm = smem + grp * kSmem;
+    Fixed &fx = reinterpret_cast<Fixed *>(smem + 2 * kSmem)[grp];
+    const int warp = wid & 3, half = (wid >> 2) & 1, r = warp * 32 + lane;
+    const bool lead = ti == 0;
+    const int units = a.H * (a.dv / PW), per = a.dv / PW, chunks = seg / Q;
+    const int64_t sall = (int64_t)a.H * DK * a.dv;
+    auto sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(kNT) : "memory"); };
+    auto x_tile = [&](int n) { return sm + (n & 1 ? kOffX : kOffF); };
+    uint64_t *b_bar = &fx.bar[2], *mma_bar = &fx.bar[3];   // and bar[0], bar[1]: X of even and odd chunks
+
+    if (lead) {
+        for (int i = 0; i < 4; ++i) mbar_init(&fx.bar[i], 1);
+        fx.bad = 0;
+        fence_mbar_init();
+    }
+    if (wid == 1) tmem_alloc(&tmem, 256);
+    if (DK < 128) {   // B^T has 128 rows: the missing key rows are zero
+        for (int i = ti; i < kBlk / 16; i += kNT)
+            reinterpret_cast<uint4 *>(sm + kOffB + kBlk)[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    fence_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = tmem + grp * 128, tl = tm + ((uint32_t)warp << 21);   // this warp's lanes: 32 warp
+
+    int n = 0;   // chunks so far: the barriers' phases
+    // The second group starts half a chunk behind the first.
+    if (grp == 1) asm volatile("bar.sync 5, %0;" ::"n"(2 * kNT) : "memory");
+    for (int64_t at = 2 * (int64_t)blockIdx.x + grp; at < items; at += 2 * (int64_t)gridDim.x) {
+        const int z = (int)(at / units), u = (int)(at - (int64_t)z * units), h = u / per, c0 = (u % per) * PW;
+        Piece p;
+        if (!find_cut(a.r, seg, z, p)) continue;
+        const int g = (int)((int64_t)h * a.G / a.H), t_first = p.j * seg;
+        const int tm_t = a.r.cu ? (int)p.row0 : 0, tm_b = a.r.cu ? 0 : p.b;
+        const unsigned short *dp = static_cast<const unsigned short *>(a.dt) + h;
+        const float A2 = a.A[h] * 1.4426950408889634f;   // log2 decay per unit step
+        const float bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
+        auto load_x = [&](int i, int nth) {   // chunk i of the piece, the nth of all
+            mbar_arrive_expect_tx(&fx.bar[nth & 1], kBlk);
+            tma_rows(x_tile(nth), &maps.x, h * a.dv + c0, tm_b, tm_t + t_first + i * Q, &fx.bar[nth & 1]);
+        };
+        if (tma && lead) {
+            load_x(0, n);
+            if (chunks > 1) load_x(1, n + 1);
+        }
+        auto raw_step = [&](int i) -> unsigned short {
+            return i < chunks ? dp[(p.row0 + (int64_t)(t_first + i * Q + r) * p.step) * a.lddt] : (unsigned short)0;
+        };
+        float d_next = 0.0f, wr = 0.0f, keep = 0.0f;
+        long long gw_next = 0, gsum = 0;
+        auto scan_steps = [&](unsigned short raw, int odd) {
+            d_next = bf16_to_f(raw) + bias;
+            if (a.softplus) d_next = softplus_f(d_next);
+            gw_next = warp_scan(decay_of(d_next, A2));
+            if (half == 0 && lane == 31) fx.wsum[odd][warp] = gw_next;
+        };
+        auto finish_steps = [&](int odd) {
+            long long base = 0, total = 0;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const long long s = fx.wsum[odd][w];
+                if (w < warp) base += s;
+                total += s;
+            }
+            wr = d_next * exp2f(decay_f(total - base - gw_next));
+            keep = exp2f(decay_f(total));
+            gsum += total;
+        };
+        float S[HW];   // the state's key row r, this thread's columns
+#pragma unroll
+        for (int i = 0; i < HW; ++i) S[i] = 0.0f;
+        // S <- decay S + the products of a chunk
+        auto update = [&](int nth, float k) {
+            tc_fence_after();
+#pragma unroll
+            for (int q = 0; q < HW; q += 16) {
+                uint32_t v[16];
+                tmem_ld_32x32b<16>(tl + (nth & 1) * PW + half * HW + q, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    const float2 s = ffma2(f2(k, k), f2(S[q + i], S[q + i + 1]),
+                                           f2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
+                    S[q + i] = s.x;
+                    S[q + i + 1] = s.y;
+                }
+            }
+            tc_fence_before();
+        };
+        const unsigned short raw0 = raw_step(0);
+        unsigned short raw = raw_step(1);
+        scan_steps(raw0, 0);
+        sync();
+        finish_steps(0);
+        scan_steps(raw, 1);
+        float keep_before = 0.0f;
+        for (int i = 0; i < chunks; ++i, ++n) {
+            raw = raw_step(i + 2);
+            // the chunk before has left X' and B
+            if (i > 0 && !mbar_wait_bounded(mma_bar, (n - 1) & 1, nullptr)) fx.bad = 1;
+            if (tma) {
+                if (lead) {
+                    mbar_arrive_expect_tx(b_bar, (DK / 64) * kBlk);
+#pragma unroll
+                    for (int j = 0; j < DK / 64; ++j)
+                        tma_rows(sm + kOffB + j * kBlk, &maps.b, g * DK + 64 * j, tm_b, tm_t + t_first + i * Q, b_bar);
+                }
+                if (!mbar_wait_bounded(&fx.bar[n & 1], (n >> 1) & 1, nullptr)) fx.bad = 1;
+            } else {
+                const int t0 = t_first + i * Q;
+                copy_tile(sm + kOffB, DK / 8, static_cast<const bf16 *>(a.Bm) + g * DK, a.ldb, p, t0, ti);
+                copy_tile(x_tile(n), PW / 8, static_cast<const bf16 *>(a.x) + (int64_t)h * a.dv + c0, a.ldx, p, t0, ti);
+                sync();
+            }
+            __syncwarp();
+            split_x(sm, x_tile(n), r, half, wr);
+            fence_async_smem();
+            tc_fence_before();
+            sync();
+            if (n == 0 && grp == 0) asm volatile("bar.arrive 5, %0;" ::"n"(2 * kNT) : "memory");
+            if (lead) {
+                if (tma && !mbar_wait_bounded(b_bar, n & 1, nullptr)) fx.bad = 1;
+                tc_fence_after();
+                const uint64_t bd = desc_mn(sm + kOffB), wd = desc_mn(sm + kOffXw);
+#pragma unroll
+                for (int part = 0; part < 3; ++part)
+#pragma unroll
+                    for (int k = 0; k < Q / 16; ++k)
+                        mma_ss(tm + (n & 1) * PW, bd + step_mn(k), wd + (part * kBlk >> 4) + step_mn(k),
+                               idesc(PW, 1, 1), part + k > 0);
+                umma_commit(mma_bar);
+                if (tma && i + 2 < chunks) load_x(i + 2, n + 2);   // (X of this chunk has been read)
+            }
+            __syncwarp();
+            if (i > 0) update(n - 1, keep_before);
+            keep_before = keep;
+            if (i + 1 < chunks) {
+                finish_steps((i + 1) & 1);
+                scan_steps(raw, i & 1);
+            }
+        }
+        if (!mbar_wait_bounded(mma_bar, (n - 1) & 1, nullptr)) fx.bad = 1;
+        __syncwarp();
+        update(n - 1, keep_before);
+        sync();   // every wait is over
+        if (r < DK) {
+            float4 *so = reinterpret_cast<float4 *>(a.ws + p.id * sall + ((int64_t)h * DK + r) * a.dv + c0 + half * HW);
+            const float nan = __int_as_float(0x7fffffff);   // a wait that ran out leaves no state that looks like one
+#pragma unroll
+            for (int i = 0; i < HW / 4; ++i)
+                so[i] = fx.bad ? make_float4(nan, nan, nan, nan)
+                               : make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+        }
+        if (ti == 0 && c0 == 0) ssm_decays(a, seg)[p.id * a.H + h] = exp2f(decay_f(gsum));
+        if (fx.bad) break;
+    }
+    if (n == 0 && grp == 0) asm volatile("bar.arrive 5, %0;" ::"n"(2 * kNT) : "memory");
+    tc_fence_before();
+    __syncthreads();
+    if (wid == 1) {
+        tmem_relinquish();
+        tmem_dealloc(tmem, 256);
     }
 }
 
@@ -780,18 +968,17 @@ cudaError_t launch(const SsmArgs &a, const SsmMaps &maps, int seg, int tma, int 
     static_assert(bytes <= 226 * 1024, "shared memory of one CTA");
     const int64_t units = (int64_t)a.H * (a.dv / PW);
     auto grid = [](int64_t items) { return (unsigned)(items < 2 * kSms ? (items + 1) / 2 : kSms); };
-    cudaError_t e = cudaFuncSetAttribute(ssm_umma_kernel<true, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t e = cudaFuncSetAttribute(ssm_umma_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     if (split) {
-        e = cudaFuncSetAttribute(ssm_umma_kernel<false, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        e = cudaFuncSetAttribute(ssm_state_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
         const int64_t cuts = cut_count(a.r, seg) * units;
-        ssm_umma_kernel<false, DK><<<grid(cuts), 2 * kNT, bytes, s>>>(a, maps, seg, (int)cuts, tma, split);
+        ssm_state_kernel<DK><<<grid(cuts), 2 * kNT, bytes, s>>>(a, maps, seg, cuts, tma);
         e = launch_ssm_join(a, seg, s);
         if (e != cudaSuccess) return e;
     }
-    const int64_t items = piece_count(a.r, seg) * units;
-    ssm_umma_kernel<true, DK><<<grid(items), 2 * kNT, bytes, s>>>(a, maps, seg, (int)items, tma, split);
+    ssm_umma_kernel<DK><<<grid(piece_count(a.r, seg) * units), 2 * kNT, bytes, s>>>(a, maps, seg, tma, split);
     return cudaGetLastError();
 }
 
