@@ -147,15 +147,18 @@ __global__ void __launch_bounds__(256) ssm_join_kernel(SsmArgs a, int seg, int c
     }
 }
 
-// Tokens per piece: pieces are cut so that the batch gives about as many
-// workers as the GPU runs side by side -- `workers` per piece (bf16: 64 value
-// columns of a head, two to an SM; else a head, two CTAs to an SM).  A batch
-// with enough sequences and heads is cut only where a sequence is longer than
-// a worker's share of all tokens.
-int piece_tokens(const Rows &r, int dtype, int H, int dv) {
-    const int64_t workers = dtype == kBF16 ? (int64_t)H * dv / 64 : H, slots = 148 * 2;
-    const int64_t share = workers <= slots ? (r.rows + slots / workers - 1) / (slots / workers)
-                                           : (r.rows * workers + slots - 1) / slots;
+// Tokens per piece: pieces are cut so that the batch gives about as many CTAs
+// as the GPU runs side by side -- for bf16 one per SM and 128 value columns, else
+// two per SM and a head each.  A batch with enough sequences and heads is cut
+// only where a sequence is longer than a CTA's share of all tokens.
+int piece_tokens(const Rows &r, int dtype, int H, int G, int dv) {
+    int64_t units = H, slots = 148 * 2;
+    if (dtype == kBF16) {
+        slots = 148;
+        if (dv == 64) units = (int64_t)G * ((H / G + 1) / 2);
+    }
+    const int64_t share = units <= slots ? (r.rows + slots / units - 1) / (slots / units)
+                                         : (r.rows * units + slots - 1) / slots;
     const int64_t seg = (share + 127) / 128 * 128;
     return (int)(seg < 128 ? 128 : seg > (1 << 30) ? (1 << 30) : seg);
 }
@@ -178,7 +181,7 @@ constexpr int kShort = 16;
 
 size_t ssm_ws_bytes(int dtype, int B, int rows, int H, int G, int dk, int dv) {
     Rows r{nullptr, B, rows};
-    const int seg = piece_tokens(r, dtype, H, dv);
+    const int seg = piece_tokens(r, dtype, H, G, dv);
     if (rows <= seg) return 0;
     // packed: at most rows / seg + B pieces, no fewer than time-major ones
     return ((size_t)(rows / seg + B) * H * (dk * dv + 1) * 4 + 255) / 256 * 256;
@@ -186,7 +189,7 @@ size_t ssm_ws_bytes(int dtype, int B, int rows, int H, int G, int dk, int dv) {
 
 cudaError_t launch_ssm_prefill(const SsmArgs &a, int dtype, cudaStream_t s) {
     if ((a.r.cu ? a.r.rows : a.r.rows / a.r.B) <= kShort) return launch_ssm_step(a, dtype, s);
-    const int seg = piece_tokens(a.r, dtype, a.H, a.dv);
+    const int seg = piece_tokens(a.r, dtype, a.H, a.G, a.dv);
     if (dtype == kBF16) return launch_ssm_umma(a, seg, may_split(a.r, seg), s);
     return launch_ssm_tc(a, dtype, seg, may_split(a.r, seg), s);
 }
