@@ -103,6 +103,21 @@ __device__ __forceinline__ void tma_rows(void *dst, const CUtensorMap *map, int 
         : "memory");
 }
 
+// States: 32 columns x DK rows as 16-byte chunks of 4, swizzled like the tiles.
+__device__ __forceinline__ void tma_state(void *dst, const CUtensorMap *map, int col, int row, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(col), "r"(row), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma_store_state(const CUtensorMap *map, const void *src, int col, int row) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(col), "r"(row), "r"(smem_u32(src))
+                 : "memory");
+}
+
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
 
 // bf16 parts of a pair: returns the pair rounded to bf16 and leaves the rests.
@@ -134,8 +149,9 @@ __device__ __forceinline__ void copy_tile(unsigned char *dst, int nch, const bf1
 
 // Token rows [T][B][width] of x, B and C as 3-D maps, boxes of 64 columns x 128
 // tokens of one sequence (packed: one sequence of all rows).
+// The states as rows of dv floats, boxes of 32 columns x dk rows.
 struct alignas(64) SsmMaps {
-    CUtensorMap x, b, c;
+    CUtensorMap x, b, c, s0, ws, s_out;
 };
 
 // 128 value columns: one head of 128, or up to two heads of 64 of one group.
@@ -173,8 +189,8 @@ struct Walk {
 };
 
 struct Fixed {
-    // G done; C S done; Y done; B^T X' done; B, C and X arrived
-    uint64_t bar[7];
+    // G done; C S done; Y done; B^T X' done; B, C, X and the first state arrived
+    uint64_t bar[8];
     long long wsum[2][2][4];   // each warp's log2 decay (even, odd chunks; heads)
     uint32_t tmem;
     int bad;             // a wait ran out
@@ -183,7 +199,7 @@ struct Fixed {
     Walk walk;
     int first[2][2 * 64];   // per value column, the first token whose x is not finite
 };
-enum { kBarG, kBarCS, kBarY, kBarS, kBarB, kBarC, kBarX };
+enum { kBarG, kBarCS, kBarY, kBarS, kBarB, kBarC, kBarX, kBarS0 };
 
 // X' of token r, 32 columns from chunk j0 on, in three parts: w x.
 __device__ __forceinline__ void split_x(unsigned char *dst, unsigned char *x, int r, int j0, float w) {
@@ -289,9 +305,6 @@ __global__ void __launch_bounds__(kNT, 1)
     const int64_t sall = (int64_t)a.H * DK * DV;
 
     float S[CW];   // the state's key row r, this thread's columns
-    auto state_at = [&](const Item &it) {
-        return ((int64_t)(it.u.h + hh) * DK + r) * DV + cq * CW - hh * DV;
-    };
     auto seq_len = [&](int b) {
         return a.r.cu ? max(cu_at(a.r, b + 1) - cu_at(a.r, b), 0) : a.r.rows / a.r.B;
     };
@@ -386,6 +399,19 @@ __global__ void __launch_bounds__(kNT, 1)
         for (int j = 0; j < blocks; ++j)
             tma_rows(sm + kOffX + j * kBlk, &maps.x, it.u.h * DV + 64 * j, it.tm_b, it.tm_t + t0, &fx.bar[kBarX]);
     };
+    // A state's 32-column blocks: on the way in where X and the third part of X'
+    // go, on the way out where the first two parts went.
+    auto s_in = [&](int c) { return sm + (c < 2 ? kOffX : kOffU + 2 * kBlk) + c * kBlk; };
+    auto load_state = [&](const Item &it) {
+        const bool cut = split && it.p.n > 1;
+        if (!cut && !a.S0) return;
+        const CUtensorMap *map = cut ? &maps.ws : &maps.s0;
+        const int64_t head = (cut ? it.p.id : it.p.b) * a.H + it.u.h;
+        const int blocks = it.u.heads * (DV / CW);
+        mbar_arrive_expect_tx(&fx.bar[kBarS0], blocks * DK * 128);
+        for (int c = 0; c < blocks; ++c)
+            tma_state(s_in(c), map, c * CW % DV, (int)((head + c * CW / DV) * DK), &fx.bar[kBarS0]);
+    };
     auto wait = [&](int bar, int parity) {
         if (!mbar_wait_bounded(&fx.bar[bar], parity, nullptr)) fx.bad = 1;
     };
@@ -394,12 +420,15 @@ __global__ void __launch_bounds__(kNT, 1)
         start_walk();
         next_item(fx.item[0]);
         if (lane == 0) {
-            for (int i = 0; i < 7; ++i) mbar_init(&fx.bar[i], 1);
+            for (int i = 0; i < 8; ++i) mbar_init(&fx.bar[i], 1);
             fx.bad = 0;
             fence_mbar_init();
-            if (tma && fx.item[0].valid) {
-                load_b(fx.item[0], fx.item[0].t_first);
-                load_c(fx.item[0], fx.item[0].t_first);
+            if (fx.item[0].valid) {
+                if (tma) {
+                    load_b(fx.item[0], fx.item[0].t_first);
+                    load_c(fx.item[0], fx.item[0].t_first);
+                }
+                load_state(fx.item[0]);
             }
         }
     }
@@ -426,7 +455,7 @@ __global__ void __launch_bounds__(kNT, 1)
     // within the chunk, the token's weight in the next state, the chunk's decay.
     float gwf = 0.0f, et = 0.0f, wr = 0.0f, keep = 0.0f;
     Steps st;
-    int parity = 0;
+    int parity = 0, s_parity = 0;
 
     for (int sel = 0; fx.item[sel].valid; sel ^= 1) {
         const Item &it = fx.item[sel];
@@ -485,25 +514,26 @@ __global__ void __launch_bounds__(kNT, 1)
             }
         };
         const unsigned short raw0 = st.load(p, it.t_first + r), raw1 = st.load(p, it.t_first + Q + r);
-        {
-            const float *S0 = nullptr;
-            if (r < DK && active) {
-                if (split && p.n > 1) S0 = a.ws + p.id * sall + state_at(it);
-                else if (a.S0) S0 = a.S0 + p.b * sall + state_at(it);
-            }
-#pragma unroll
-            for (int i = 0; i < CW / 4; ++i) {
-                const float4 v = S0 ? reinterpret_cast<const float4 *>(S0)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
-                S[4 * i] = v.x; S[4 * i + 1] = v.y; S[4 * i + 2] = v.z; S[4 * i + 3] = v.w;
-            }
-        }
         scan(raw0, it.t_first + r, 0);
+        const bool given = (split && p.n > 1) || a.S0;
+        if (given) {
+            wait(kBarS0, s_parity);
+            s_parity ^= 1;
+        }
+#pragma unroll
+        for (int i = 0; i < CW / 4; ++i) {
+            const uint4 z = make_uint4(0u, 0u, 0u, 0u), v = given && r < DK && active ? *chunk(s_in(cq), r, i) : z;
+            S[4 * i] = __uint_as_float(v.x);
+            S[4 * i + 1] = __uint_as_float(v.y);
+            S[4 * i + 2] = __uint_as_float(v.z);
+            S[4 * i + 3] = __uint_as_float(v.w);
+        }
+        __syncthreads();   // the state has been read, the one before has left
         split_state();
         if (HPC == 2 && !active) {   // no second head: zeros in its place
 #pragma unroll
             for (int j = 0; j < CW / 8; ++j) *chunk(sm + kOffX, r, j0 + j) = make_uint4(0u, 0u, 0u, 0u);
         }
-        __syncthreads();
         finish(0);
         scan(raw1, it.t_first + Q + r, 1);
         for (int t0 = it.t_first; t0 < t_end; t0 += Q, parity ^= 1) {
@@ -797,18 +827,35 @@ __global__ void __launch_bounds__(kNT, 1)
             }
             if (!last) split_state();
         }
-        __syncthreads();   // the next item is known
-        // A wait that ran out leaves no state that looks like one.
-        if (r < DK && active && p.j == p.n - 1) {
-            const float nan = __int_as_float(0x7fffffff);
-            float4 *so = reinterpret_cast<float4 *>(a.S_out + p.b * sall + state_at(it));
+        // The last piece's state leaves; one after a wait that ran out does not look
+        // like a state.
+        const bool ends = p.j == p.n - 1;
+        if (ends && r < DK) {
+            const bool bad = fx.bad;
 #pragma unroll
-            for (int i = 0; i < CW / 4; ++i)
-                so[i] = fx.bad ? make_float4(nan, nan, nan, nan)
-                               : make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+            for (int i = 0; i < CW / 4; ++i) {
+                uint32_t v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = bad ? 0x7fffffffu : __float_as_uint(S[4 * i + k]);
+                *chunk(sm + kOffU + cq * kBlk, r, i) = make_uint4(v[0], v[1], v[2], v[3]);
+            }
         }
+        fence_async_smem();
+        __syncthreads();   // (and the next item is known)
+        if (finder && lane == 0) {
+            if (ends) {
+                const int64_t head = (int64_t)p.b * a.H + it.u.h;
+                for (int c = 0; c < it.u.heads * (DV / CW); ++c)
+                    tma_store_state(&maps.s_out, sm + kOffU + c * kBlk, c * CW % DV, (int)((head + c * CW / DV) * DK));
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+            if (!fx.bad && fx.item[sel ^ 1].valid) load_state(fx.item[sel ^ 1]);
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        }
+        __syncwarp();
         if (fx.bad) break;
     }
+    if (finder && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     tc_fence_before();
     __syncthreads();
     if (wid == 2) {
@@ -1000,6 +1047,16 @@ bool encode(CUtensorMap *m, const void *base, const Rows &r, int64_t width, int6
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_states(CUtensorMap *m, const float *base, int64_t heads, int dk, int dv) {
+    const auto enc = encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)dv, (cuuint64_t)heads * dk}, strides[1] = {(cuuint64_t)dv * 4};
+    const cuuint32_t box[2] = {CW, (cuuint32_t)dk}, es[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<float *>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int DK, int HPC>
 cudaError_t launch(const SsmArgs &a, const SsmMaps &maps, int seg, int tma, int split, cudaStream_t s) {
     constexpr int bytes = kOffFixed + (int)sizeof(Fixed);
@@ -1031,6 +1088,11 @@ cudaError_t launch_ssm_umma(const SsmArgs &a, int seg, bool split, cudaStream_t 
                      encode(&maps.x, a.x, a.r, (int64_t)a.H * a.dv, a.ldx) &&
                      encode(&maps.b, a.Bm, a.r, (int64_t)a.G * a.dk, a.ldb) &&
                      encode(&maps.c, a.Cm, a.r, (int64_t)a.G * a.dk, a.ldc);
+    const int64_t heads = (int64_t)a.r.B * a.H;
+    if (!encode_states(&maps.s_out, a.S_out, heads, a.dk, a.dv) ||
+        (a.S0 && !encode_states(&maps.s0, a.S0, heads, a.dk, a.dv)) ||
+        (split && !encode_states(&maps.ws, a.ws, piece_count(a.r, seg) * a.H, a.dk, a.dv)))
+        return cudaErrorNotSupported;
     if (a.dv == 128)
         return a.dk == 64 ? launch<64, 1>(a, maps, seg, tma, split, s) : launch<128, 1>(a, maps, seg, tma, split, s);
     return a.dk == 64 ? launch<64, 2>(a, maps, seg, tma, split, s) : launch<128, 2>(a, maps, seg, tma, split, s);
