@@ -866,40 +866,43 @@ __global__ void __launch_bounds__(kNT, 1)
 
 // The pieces' own states, from zero, and their decays, for every piece that is
 // followed by another (all of them seg tokens long): only B^T X' and the state
-// update.  Without C and S the tiles of X have two places, a chunk ahead, and
+// update.  Without C and S the tiles of B have two places, a chunk ahead, and
 // the products of a chunk two accumulators, so that the update runs beside the
-// next chunk's MMAs.
-//   [0, 32K) X of even chunks, [32K, 64K) B, [64K, 96K) X of odd chunks, [96K, 192K) X' parts
+// next chunk's MMAs; a 17th warp issues the copies and the MMAs.
+//   [0, 32K) B of even chunks, [32K, 64K) of odd ones, [64K, 96K) X, [96K, 192K) X' parts
 template <int DK, int HPC>
-__global__ void __launch_bounds__(kNT, 1)
+__global__ void __launch_bounds__(kNT + 32, 1)
     ssm_state_kernel(SsmArgs a, const __grid_constant__ SsmMaps maps, int seg, int64_t items, int tma) {
     constexpr int DV = 128 / HPC;
     extern __shared__ __align__(1024) unsigned char sm[];
     Fixed &fx = *reinterpret_cast<Fixed *>(sm + kOffFixed);
     const int ti = threadIdx.x, wid = ti >> 5, lane = ti & 31;
-    const int warp = wid & 3, cq = wid >> 2, r = warp * 32 + lane;
+    const int warp = wid & 3, cq = (wid >> 2) & 3, r = warp * 32 + lane;
     const int hh = HPC == 2 ? cq >> 1 : 0, j0 = cq * (CW / 8);
-    const bool lead = ti == 0, loader = ti == 32;
+    const bool issuer = wid == kNT / 32, lead = ti == kNT;
     const int units = unit_count<HPC>(a.H, a.G), chunks = seg / Q;
     const int64_t sall = (int64_t)a.H * DK * DV;
-    auto x_tile = [&](int n) { return sm + (n & 1 ? kOffX : kOffC); };
-    uint64_t *b_bar = &fx.bar[2], *mma_bar = &fx.bar[3];   // and bar[0], bar[1]: X of even and odd chunks
+    auto b_tile = [&](int n) { return sm + (n & 1 ? kOffB : kOffC); };
+    uint64_t *x_bar = &fx.bar[2], *mma_bar = &fx.bar[3];   // and bar[0], bar[1]: B of even and odd chunks
 
-    if (loader) {
+    if (lead) {
         for (int i = 0; i < 4; ++i) mbar_init(&fx.bar[i], 1);
         fx.bad = 0;
         fence_mbar_init();
     }
     if (wid == 2) tmem_alloc(&fx.tmem, 256);
     if (DK < 128) {   // B^T has 128 rows: the missing key rows are zero
-        for (int i = ti; i < kBlk / 16; i += kNT)
-            reinterpret_cast<uint4 *>(sm + kOffB + kBlk)[i] = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = ti; i < kBlk / 16; i += kNT + 32)
+            reinterpret_cast<uint4 *>(sm + kOffB + kBlk)[i] = reinterpret_cast<uint4 *>(sm + kOffC + kBlk)[i] =
+                make_uint4(0u, 0u, 0u, 0u);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = fx.tmem, tl = tm + ((uint32_t)warp << 21);   // this warp's lanes: 32 warp
 
+    // (The issuing warp meets the others at the same barriers from code of its own.)
+    auto sync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(kNT + 32) : "memory"); };
     int n = 0;   // chunks so far: the barriers' phases
     for (int64_t at = blockIdx.x; at < items; at += gridDim.x) {
         const int z = (int)(at / units);
@@ -909,21 +912,48 @@ __global__ void __launch_bounds__(kNT, 1)
         const bool active = hh < u.heads;
         const int t_first = p.j * seg;
         const int tm_t = a.r.cu ? (int)p.row0 : 0, tm_b = a.r.cu ? 0 : p.b;
-        auto load_x = [&](int i, int nth) {   // chunk i of the piece, the nth of all
+        auto load_x = [&](int i) {   // chunk i of the piece
             const int blocks = HPC == 1 ? 2 : u.heads;
-            mbar_arrive_expect_tx(&fx.bar[nth & 1], blocks * kBlk);
+            mbar_arrive_expect_tx(x_bar, blocks * kBlk);
             for (int j = 0; j < blocks; ++j)
-                tma_rows(x_tile(nth) + j * kBlk, &maps.x, u.h * DV + 64 * j, tm_b, tm_t + t_first + i * Q,
-                         &fx.bar[nth & 1]);
+                tma_rows(sm + kOffX + j * kBlk, &maps.x, u.h * DV + 64 * j, tm_b, tm_t + t_first + i * Q, x_bar);
         };
-        if (tma && loader) {
-            load_x(0, n);
-            if (chunks > 1) load_x(1, n + 1);
+        auto load_b = [&](int i, int nth) {   // the nth of all
+            uint64_t *bar = &fx.bar[nth & 1];
+            mbar_arrive_expect_tx(bar, DK / 64 * kBlk);
+#pragma unroll
+            for (int j = 0; j < DK / 64; ++j)
+                tma_rows(b_tile(nth) + j * kBlk, &maps.b, u.g * DK + 64 * j, tm_b, tm_t + t_first + i * Q, bar);
+        };
+        if (tma && lead) {
+            load_x(0);
+            load_b(0, n);
+        }
+        if (issuer) {
+            sync();
+            for (int i = 0; i < chunks; ++i, ++n) {
+                // the chunk before has left X' and its B
+                if (i > 0 && !mbar_wait_bounded(mma_bar, (n - 1) & 1, nullptr)) fx.bad = 1;
+                if (tma && lead && i + 1 < chunks) load_b(i + 1, n + 1);
+                if (!tma) sync();
+                sync();   // X' is in place
+                if (lead) {
+                    if (tma && i + 1 < chunks) load_x(i + 1);   // (X of this chunk has been read)
+                    if (tma && !mbar_wait_bounded(&fx.bar[n & 1], (n >> 1) & 1, nullptr)) fx.bad = 1;
+                    tc_fence_after();
+                    issue_state(tm + (n & 1) * 128, b_tile(n), sm + kOffU);
+                    umma_commit(mma_bar);
+                }
+                __syncwarp();
+            }
+            if (!mbar_wait_bounded(mma_bar, (n - 1) & 1, nullptr)) fx.bad = 1;
+            sync();   // every wait is over
+            if (fx.bad) break;
+            continue;
         }
         if (HPC == 2 && !active) {   // no second head: zeros in its place
 #pragma unroll
-            for (int j = 0; j < CW / 8; ++j)
-                *chunk(sm + kOffC, r, j0 + j) = *chunk(sm + kOffX, r, j0 + j) = make_uint4(0u, 0u, 0u, 0u);
+            for (int j = 0; j < CW / 8; ++j) *chunk(sm + kOffX, r, j0 + j) = make_uint4(0u, 0u, 0u, 0u);
         }
         Steps st;
         st.head(a, u.h + hh, active);
@@ -950,40 +980,26 @@ __global__ void __launch_bounds__(kNT, 1)
         const unsigned short raw0 = st.load(p, t_first + r);
         unsigned short raw = st.load(p, t_first + Q + r);
         scan(raw0, true, 0);
-        __syncthreads();
+        sync();
         finish(0);
         scan(raw, chunks > 1, 1);
         for (int i = 0; i < chunks; ++i, ++n) {
             raw = st.load(p, t_first + (i + 2) * Q + r);
-            // the chunk before has left X' and B
+            // the chunk before has left X'
             if (i > 0 && !mbar_wait_bounded(mma_bar, (n - 1) & 1, nullptr)) fx.bad = 1;
             if (tma) {
-                if (loader) {
-                    mbar_arrive_expect_tx(b_bar, DK / 64 * kBlk);
-#pragma unroll
-                    for (int j = 0; j < DK / 64; ++j)
-                        tma_rows(sm + kOffB + j * kBlk, &maps.b, u.g * DK + 64 * j, tm_b, tm_t + t_first + i * Q, b_bar);
-                }
-                if (!mbar_wait_bounded(&fx.bar[n & 1], (n >> 1) & 1, nullptr)) fx.bad = 1;
+                if (!mbar_wait_bounded(x_bar, n & 1, nullptr)) fx.bad = 1;
             } else {
                 const int t0 = t_first + i * Q;
-                copy_tile(sm + kOffB, DK / 8, static_cast<const bf16 *>(a.Bm) + u.g * DK, a.ldb, p, t0);
-                copy_tile(x_tile(n), u.heads * (DV / 8), static_cast<const bf16 *>(a.x) + (int64_t)u.h * DV, a.ldx, p, t0);
-                __syncthreads();
+                copy_tile(b_tile(n), DK / 8, static_cast<const bf16 *>(a.Bm) + u.g * DK, a.ldb, p, t0);
+                copy_tile(sm + kOffX, u.heads * (DV / 8), static_cast<const bf16 *>(a.x) + (int64_t)u.h * DV, a.ldx, p, t0);
+                sync();
             }
             __syncwarp();
-            split_x(sm + kOffU, x_tile(n), r, j0, wr);
+            split_x(sm + kOffU, sm + kOffX, r, j0, wr);
             fence_async_smem();
             tc_fence_before();
-            __syncthreads();
-            if (lead) {
-                if (tma && !mbar_wait_bounded(b_bar, n & 1, nullptr)) fx.bad = 1;
-                tc_fence_after();
-                issue_state(tm + (n & 1) * 128, sm + kOffB, sm + kOffU);
-                umma_commit(mma_bar);
-            }
-            if (loader && tma && i + 2 < chunks) load_x(i + 2, n + 2);   // (X of this chunk has been read)
-            __syncwarp();
+            sync();
             if (i > 0) {
                 tc_fence_after();
                 update_state(S, tl + ((n - 1) & 1) * 128 + cq * CW, keep_before);
@@ -1000,7 +1016,7 @@ __global__ void __launch_bounds__(kNT, 1)
         tc_fence_after();
         update_state(S, tl + ((n - 1) & 1) * 128 + cq * CW, keep_before);
         tc_fence_before();
-        __syncthreads();   // every wait is over
+        sync();   // every wait is over
         if (r < DK && active) {
             float4 *so = reinterpret_cast<float4 *>(a.ws + p.id * sall + ((int64_t)(u.h + hh) * DK + r) * DV + cq * CW -
                                                     hh * DV);
@@ -1069,7 +1085,7 @@ cudaError_t launch(const SsmArgs &a, const SsmMaps &maps, int seg, int tma, int 
         e = cudaFuncSetAttribute(ssm_state_kernel<DK, HPC>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
         const int64_t cuts = cut_count(a.r, seg) * units;
-        ssm_state_kernel<DK, HPC><<<grid(cuts), kNT, bytes, s>>>(a, maps, seg, cuts, tma);
+        ssm_state_kernel<DK, HPC><<<grid(cuts), kNT + 32, bytes, s>>>(a, maps, seg, cuts, tma);
         e = launch_ssm_join(a, seg, s);
         if (e != cudaSuccess) return e;
     }
