@@ -90,3 +90,38 @@ GDN_DAMP = Workload(
 
 WORKLOADS = [TINY_GDN, GDN_SERVING, KDA_B256, GDN_PREFIX_CACHE, GDN_DAMP]
 BY_NAME = {w.name: w for w in WORKLOADS}
+
+
+@dataclass(frozen=True)
+class ScanLayer:
+    """Sizes of one selective-scan layer (runner.ScanRunner): model width d, H
+    heads of dv value columns, G groups of B and C of dk, K convolution taps."""
+    name: str
+    d: int
+    H: int
+    G: int
+    dk: int
+    dv: int
+    K: int = 4
+    eps: float = 1e-5
+    scale: float = 1.0           # residual scale of the block before
+    dt_lo: float = 1e-3          # initial steps, log-uniform
+    dt_hi: float = 1e-1
+    seed: int = 0
+
+    @property
+    def inner(self) -> int:
+        return self.H * self.dv
+
+    @property
+    def conv(self) -> int:
+        return self.inner + 2 * self.G * self.dk
+
+    @property
+    def proj(self) -> int:       # columns of the input projection: z, x | B | C, dt
+        return self.inner + self.conv + self.H
+
+
+# A scan layer beside the tiny workload's heads, and one of 16 heads of 128.
+TINY_SCAN = ScanLayer(name="scan_tiny_d96_h2_g1_dk64_dv64", d=96, H=2, G=1, dk=64, dv=64)
+SCAN_LAYER = ScanLayer(name="scan_d1024_h16_g1_dk128_dv128", d=1024, H=16, G=1, dk=128, dv=128)

@@ -9,11 +9,13 @@ memory, the seeded input draws (inputs.py), streams and CUDA graphs.
 """
 from __future__ import annotations
 
+import math
+
 import torch
 
 from . import inputs as gen
 from . import lq
-from .configs import Workload
+from .configs import ScanLayer, Workload
 
 
 def gpu_prefill(wl: Workload, *, tokens: int | None = None, batch: int | None = None, stream: str = "prefill",
@@ -158,3 +160,91 @@ class WindowRunner:
 
     def replay(self, w: int):
         self.graphs[w % self.n_windows].replay()
+
+
+def scan_weights(sl: ScanLayer, dtype=torch.bfloat16, device="cuda") -> dict:
+    """Seeded weights of a scan layer: the two projections in the activations'
+    type, everything else float32.  The steps' bias is the inverse softplus of
+    steps log-uniform in [dt_lo, dt_hi], the decays' rates A uniform in -[1, 16]."""
+    g = torch.Generator(device=device).manual_seed(sl.seed)
+    randn = lambda *s: torch.randn(s, generator=g, device=device)   # noqa: E731
+    rand = lambda *s: torch.rand(s, generator=g, device=device)     # noqa: E731
+    step = torch.exp(math.log(sl.dt_lo) + rand(sl.H) * math.log(sl.dt_hi / sl.dt_lo))
+    return {"w_norm": 1 + 0.1 * randn(sl.d),
+            "w_in": (randn(sl.d, sl.proj) * sl.d ** -0.5).to(dtype),
+            "w_conv": randn(sl.conv, sl.K) * sl.K ** -0.5, "b_conv": 0.1 * randn(sl.conv),
+            "A": -(1 + 15 * rand(sl.H)), "D": torch.ones(sl.H, device=device),
+            "dt_bias": step + torch.log(-torch.expm1(-step)),
+            "w_gate": 1 + 0.1 * randn(sl.dv),
+            "w_out": (randn(sl.inner, sl.d) * sl.inner ** -0.5).to(dtype)}
+
+
+class ScanRunner:
+    """One selective-scan layer for a batch of B sequences, prompts and single
+    tokens: norm with the residual (lq_norm_in), input projection, short
+    convolution (lq_conv_*), scan (lq_ssm_*), gated norm per head (lq_norm_out),
+    output projection.  The projections are plain library products; all else
+    runs in liblq.so.  Holds the sequences' convolution windows and states."""
+
+    def __init__(self, sl: ScanLayer, B: int, dtype=torch.bfloat16, device="cuda", weights=None):
+        self.sl, self.B, self.dtype = sl, B, dtype
+        self.w = scan_weights(sl, dtype, device) if weights is None else weights
+        self.window = torch.zeros((B, sl.K - 1, sl.conv), dtype=dtype, device=device)
+        self.state = torch.zeros((B, sl.H, sl.dk, sl.dv), device=device)
+        self.graph = None
+
+    def _split(self, p: torch.Tensor):
+        """z, convolution inputs and steps: columns of the projection."""
+        n, c = self.sl.inner, self.sl.conv
+        return p[..., :n].unflatten(-1, (self.sl.H, self.sl.dv)), p[..., n:n + c], p[..., n + c:]
+
+    def _heads(self, xbc: torch.Tensor):
+        n, gk = self.sl.inner, self.sl.G * self.sl.dk
+        return (xbc[..., :n].unflatten(-1, (self.sl.H, self.sl.dv)),
+                xbc[..., n:n + gk].unflatten(-1, (self.sl.G, self.sl.dk)),
+                xbc[..., n + gk:].unflatten(-1, (self.sl.G, self.sl.dk)))
+
+    def prompt(self, x: torch.Tensor, res=None, cu=None):
+        """Tokens of all sequences, x [rows, d] with cu or [T, B, d], from the
+        windows and states held, which move on.  Returns (block output,
+        residual): the next block's norm adds them."""
+        sl, w = self.sl, self.w
+        u, h = lq.lq_norm_in(x, w["w_norm"], res=res, scale=sl.scale, eps=sl.eps)
+        z, xbc, dt = self._split(u @ w["w_in"])
+        xbc, _ = lq.lq_conv_prefill(xbc, w["w_conv"], w["b_conv"], state0=self.window, state_out=self.window, cu=cu)
+        xs, Bm, Cm = self._heads(xbc)
+        y, _ = lq.lq_ssm_prefill(xs, dt, w["A"], Bm, Cm, D=w["D"], dt_bias=w["dt_bias"], S0=self.state,
+                                 S_out=self.state, cu=cu)
+        y = lq.lq_norm_out(y, w["w_gate"], z=z, eps=sl.eps, y=y)
+        return y.flatten(-2) @ w["w_out"], h
+
+    def step(self, x: torch.Tensor, res=None):
+        """One token of every sequence, x [B, d]."""
+        sl, w = self.sl, self.w
+        u, h = lq.lq_norm_in(x, w["w_norm"], res=res, scale=sl.scale, eps=sl.eps)
+        z, xbc, dt = self._split(u @ w["w_in"])
+        xs, Bm, Cm = self._heads(lq.lq_conv_step(self.window, xbc, w["w_conv"], w["b_conv"]))
+        y = lq.lq_ssm_step(self.state, xs, dt, w["A"], Bm, Cm, D=w["D"], dt_bias=w["dt_bias"])
+        y = lq.lq_norm_out(y, w["w_gate"], z=z, eps=sl.eps, y=y)
+        return y.flatten(-2) @ w["w_out"], h
+
+    def capture(self):
+        """A CUDA graph of one step on fixed buffers: fill x_in (and res_in), call
+        replay(), read the returned (out, residual)."""
+        keep = self.window.clone(), self.state.clone()
+        self.x_in = torch.zeros((self.B, self.sl.d), dtype=self.dtype, device=self.window.device)
+        self.res_in = torch.zeros_like(self.x_in)
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            self.step(self.x_in, self.res_in)      # warm the launch path before capture
+        torch.cuda.current_stream().wait_stream(s)
+        self.graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(self.graph):
+            self.out = self.step(self.x_in, self.res_in)
+        self.window.copy_(keep[0])
+        self.state.copy_(keep[1])
+
+    def replay(self):
+        self.graph.replay()
+        return self.out

@@ -18,7 +18,7 @@ import math
 import pytest
 import torch
 
-from quantized_recurrent_state_lq_b200 import lq
+from quantized_recurrent_state_lq_b200 import configs, inputs as gen, lq, runner
 from tests import layer_ref as R
 
 pytestmark = pytest.mark.gpu
@@ -425,3 +425,106 @@ def test_same_inputs_same_bits():
         cu = _cu([1300, 200])
         a = [lq.lq_ssm_prefill(v["x"], v["dt"], v["A"], v["Bm"], v["Cm"], S0=v["S0"], cu=cu) for _ in range(3)]
         assert all(torch.equal(a[0][i], b[i]) for b in a[1:] for i in range(2))
+
+
+def _scan_layer_ref(sl, w, x, res, lens):
+    """The layer of ScanRunner in 64 bits over packed sequences."""
+    f = {k: v.double() for k, v in w.items()}
+    u, h = R.norm_in(x, f["w_norm"], res, sl.scale, sl.eps)
+    p = u @ f["w_in"]
+    cu = _cu(lens)
+    n, gk = sl.inner, sl.G * sl.dk
+    xbc, win, _ = R.conv(p[:, n:n + sl.conv], f["w_conv"], f["b_conv"], "silu", None, cu)
+    y, S, _, _, _ = R.ssm(xbc[:, :n].unflatten(-1, (sl.H, sl.dv)), p[:, n + sl.conv:], f["A"],
+                          xbc[:, n:n + gk].unflatten(-1, (sl.G, sl.dk)), xbc[:, n + gk:].unflatten(-1, (sl.G, sl.dk)),
+                          f["D"], f["dt_bias"], True, None, cu)
+    y = R.norm_out(y, f["w_gate"], p[:, :n].unflatten(-1, (sl.H, sl.dv)), "silu", False, None, 1.0, sl.eps)
+    return y.flatten(-2) @ f["w_out"], h, win, S
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+def test_scan_layer_prompts_then_tokens(dtype):
+    """ScanRunner: ragged prompts, then single tokens, eager and from a captured
+    graph, against the whole sequences in 64 bits.  Every stage rounds its
+    output once and the stages after it carry that on: 12 half steps of the type
+    relative to the largest value of each output (two projections, two norms,
+    convolution, scan, gate; sums of random-sign errors), plus 1e-5."""
+    _gpu()
+    sl = configs.TINY_SCAN
+    lens, more = [70, 1, 133], 4
+    g = _gen(21)
+    x = _randn(g, (sum(lens) + 3 * more, sl.d), dtype)
+    res = _randn(g, x.shape, dtype)
+    # rows of each sequence: its prompt, then its single tokens
+    prompt, steps, at = [], [[] for _ in range(more)], 0
+    for n in lens:
+        prompt += range(at, at + n)
+        for i in range(more):
+            steps[i].append(at + n + i)
+        at += n + more
+    run = runner.ScanRunner(sl, 3, dtype)
+    out, h = torch.empty_like(x), torch.empty_like(x)
+    out[prompt], h[prompt] = run.prompt(x[prompt], res[prompt], cu=_cu(lens))
+    for i in range(more):
+        if i == 2:
+            run.capture()
+        if i < 2:
+            out[steps[i]], h[steps[i]] = run.step(x[steps[i]], res[steps[i]])
+        else:
+            run.x_in.copy_(x[steps[i]])
+            run.res_in.copy_(res[steps[i]])
+            out[steps[i]], h[steps[i]] = run.replay()
+    ro, rh, rw, rS = _scan_layer_ref(sl, run.w, x, res, [n + more for n in lens])
+    for name, got, want in (("out", out, ro), ("residual", h, rh), ("window", run.window, rw), ("state", run.state, rS)):
+        off = (got.double() - want).abs().max().item() / want.abs().max().item()
+        print(f"scan layer {ids(dtype)} {name}: {off:.2e}")
+        assert off <= 12 * R.half_step(dtype) + 1e-5, (name, off)
+
+
+def test_delta_rule_layer_around_the_windowed_state():
+    """The operators around the library's own recurrence, as a delta-rule layer
+    uses them: convolution, L2 norm of q and k, prefill, the quantized windowed
+    state, decode steps, gated norm of their float32 outputs -- the convolution
+    and norms against 64 bits at every token, and the decode against the FP32
+    state's decode on the same inputs (the quantized state's own error is the
+    windowed decode's subject)."""
+    _gpu()
+    wl = configs.TINY_GDN.with_(B=2, W=4, T=8)
+    B, H, d, T = wl.B, wl.H, wl.dk, 20
+    g = _gen(31)
+    C = 3 * H * d
+    raw = _randn(g, (T + 8, B, C + H * d), F32)           # q | k | v and the gate's columns
+    w, bias = _randn(g, (C, 4), scale=0.5), _randn(g, (C,), scale=0.1)
+    wn, wl2 = 1 + _randn(g, (d,), scale=0.1), torch.full((d,), d ** -0.5, device="cuda")
+    tok = gen.token_inputs(wl, T + 8, device="cuda")
+    xs, window = lq.lq_conv_prefill(raw[:T, :, :C], w, bias)
+    tail = torch.stack([lq.lq_conv_step(window, raw[t, :, :C], w, bias) for t in range(T, T + 8)])
+    xs = torch.cat([xs, tail])
+    ry, _, mag = R.conv(raw[..., :C], w, bias, "silu", None, None)
+    _close(xs, ry, _conv_tol(ry, mag, F32, 4, "silu"), "delta layer convolution")
+    q, k, v = (t.unflatten(-1, (H, d)) for t in xs.split(H * d, -1))
+    unit = [lq.lq_norm_out(t.contiguous(), wl2, eps=1e-12) for t in (q, k)]
+    for t, n in zip((q, k), unit):
+        want = t.double() / torch.linalg.vector_norm(t.double(), dim=-1, keepdim=True)
+        _close(n, want, 1e-6 * want.abs() + 1e-9, "L2 norm")
+    q, k, v = unit[0], unit[1], v.contiguous()
+    outs = {}
+    for mode in ("fp32", "window"):
+        cfg = lq.Config.from_workload(wl, mode=mode)
+        S = lq.lq_prefill(cfg, q[:T], k[:T], v[:T], tok["beta"][:T], tok["alpha"][:T])
+        st = lq.lq_state_init(cfg, S)
+        o = torch.empty((8, B, H, d), device="cuda")
+        for i in range(8):
+            t = T + i
+            lq.lq_decode_step(st, q[t], k[t], v[t], tok["beta"][t].contiguous(), tok["alpha"][t].contiguous(), o[i])
+        assert lq.lq_get_status(st) == lq.LQ_OK
+        z = raw[T:, :, C:].unflatten(-1, (H, d)).to(BF16)
+        y = lq.lq_norm_out(o, wn, z=z, eps=1e-6)
+        assert y.dtype == BF16
+        ref = R.norm_out(o, wn, z, "silu", False, None, 1.0, 1e-6)
+        _close(y, ref, _norm_tol(ref, ref.abs(), BF16, d, "silu"), f"delta layer gate {mode}")
+        outs[mode] = y.double()
+    # an 8-bit state: a step of the codes is amax / 127 of a column
+    off = (outs["window"] - outs["fp32"]).norm() / outs["fp32"].norm()
+    print(f"delta layer, windowed against FP32 state: {off:.2e}")
+    assert off < 0.05
