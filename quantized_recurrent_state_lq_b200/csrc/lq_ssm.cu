@@ -175,9 +175,15 @@ cudaError_t launch_ssm_join(const SsmArgs &a, int seg, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-// A prompt whose sequences are this short runs token by token: a chunk costs
-// about as much (10 us) whatever it holds, a token 0.5 us.
-constexpr int kShort = 16;
+// Whether a prompt runs token by token.  A chunk costs about as much (7 to 10 us)
+// whatever it holds, a token 0.5 us: so do sequences of at most 16 tokens, and
+// packed batches of at most 2 tokens a sequence on average and 512 in all (64
+// single tokens of 32 heads of 128 x 128: 50 us against 155), where one long
+// sequence costs no more than 512 steps.
+bool token_by_token(const Rows &r) {
+    if (!r.cu) return r.rows / r.B <= 16;
+    return r.rows <= 16 || (r.rows <= 2 * (int64_t)r.B && r.rows <= 512);
+}
 
 size_t ssm_ws_bytes(int dtype, int B, int rows, int H, int G, int dk, int dv) {
     Rows r{nullptr, B, rows};
@@ -188,7 +194,7 @@ size_t ssm_ws_bytes(int dtype, int B, int rows, int H, int G, int dk, int dv) {
 }
 
 cudaError_t launch_ssm_prefill(const SsmArgs &a, int dtype, cudaStream_t s) {
-    if ((a.r.cu ? a.r.rows : a.r.rows / a.r.B) <= kShort) return launch_ssm_step(a, dtype, s);
+    if (token_by_token(a.r)) return launch_ssm_step(a, dtype, s);
     const int seg = piece_tokens(a.r, dtype, a.H, a.G, a.dv);
     if (dtype == kBF16) return launch_ssm_umma(a, seg, may_split(a.r, seg), s);
     return launch_ssm_tc(a, dtype, seg, may_split(a.r, seg), s);

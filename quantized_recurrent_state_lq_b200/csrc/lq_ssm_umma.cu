@@ -311,25 +311,46 @@ __global__ void __launch_bounds__(kNT, 1)
     // (Both by the second warp.)  The first item that starts in this CTA's part.
     auto start_walk = [&]() {
         Walk w{};
-        int64_t all = 0;
-        for (int b = lane; b < a.r.B; b += 32) all += (seq_len(b) + Q - 1) / Q;
-        all = warp_scan(all);
-        all = __shfl_sync(0xffffffffu, all, 31) * units;
-        w.pos = all * blockIdx.x / gridDim.x;
-        w.end = all * (blockIdx.x + 1) / gridDim.x;
+        auto seq_chunks = [&](int b) { return b < a.r.B ? (seq_len(b) + Q - 1) / Q : 0; };
         int64_t before = 0;   // chunks of the sequences before b
         w.b = a.r.B;
-        for (int b0 = 0; b0 < a.r.B; b0 += 32) {
-            const int64_t n = b0 + lane < a.r.B ? (int64_t)((seq_len(b0 + lane) + Q - 1) / Q) * units : 0;
-            const int64_t upto = before + warp_scan(n);
-            const unsigned in = __ballot_sync(0xffffffffu, upto > w.pos);
-            if (in) {   // the sequence that holds the first position
-                const int l = __ffs(in) - 1;
-                w.b = b0 + l;
-                before = __shfl_sync(0xffffffffu, upto - n, l);
-                break;
+        if (!a.r.cu) {
+            const int64_t each = (int64_t)seq_chunks(0) * units, all = each * a.r.B;
+            w.pos = all * blockIdx.x / gridDim.x;
+            w.end = all * (blockIdx.x + 1) / gridDim.x;
+            if (w.pos < all) w.b = (int)(w.pos / each);
+            before = w.b * each;
+        } else {
+            // The whole batch's chunks, then the sequence that holds the first
+            // position: 8 sequences per lane and step.
+            int64_t all = 0;
+            for (int b0 = 0; b0 < a.r.B; b0 += 256)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) all += seq_chunks(b0 + 8 * lane + i);
+            all = warp_scan(all);
+            all = __shfl_sync(0xffffffffu, all, 31) * units;
+            w.pos = all * blockIdx.x / gridDim.x;
+            w.end = all * (blockIdx.x + 1) / gridDim.x;
+            for (int b0 = 0; b0 < a.r.B; b0 += 256) {
+                int64_t n = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) n += (int64_t)seq_chunks(b0 + 8 * lane + i) * units;
+                const int64_t upto = before + warp_scan(n);
+                const unsigned in = __ballot_sync(0xffffffffu, upto > w.pos);
+                if (in) {
+                    const int l = __ffs(in) - 1;
+                    before = __shfl_sync(0xffffffffu, upto - n, l);
+                    w.b = b0 + 8 * l;
+                    for (;;) {
+                        const int64_t c = (int64_t)seq_chunks(w.b) * units;
+                        if (before + c > w.pos) break;
+                        before += c;
+                        ++w.b;
+                    }
+                    break;
+                }
+                before = __shfl_sync(0xffffffffu, upto, 31);
             }
-            before = __shfl_sync(0xffffffffu, upto, 31);
         }
         if (w.b < a.r.B) {
             const int len = seq_len(w.b), n = (len + seg - 1) / seg, whole = seg / Q;

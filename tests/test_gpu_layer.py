@@ -316,6 +316,77 @@ def test_ssm_rows_outside_the_sequences_stay():
         assert (y[:7] == 7).all() and (y[280:] == 7).all() and not (y[7:280] == 7).all(-1).any()
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+def test_ssm_many_short_sequences(dtype):
+    """More sequences than a warp looks at in one step, of 0 to 40 tokens."""
+    _gpu()
+    lens = [(i * 37) % 41 if i % 5 else 0 for i in range(700)]
+    cu = _cu(lens)
+    v = _ssm_inputs(17, (int(cu[-1]),), len(lens), 2, 1, 64, 64, dtype)
+    y, S = lq.lq_ssm_prefill(v["x"], v["dt"], v["A"], v["Bm"], v["Cm"], D=v["D"], dt_bias=v["dt_bias"], S0=v["S0"], cu=cu)
+    at = cu.tolist()
+    for b in (0, 1, 31, 32, 255, 256, 257, 511, 512, 698, 699):
+        one = slice(at[b], at[b + 1])
+        part = {k: (w[one] if k in ("x", "dt", "Bm", "Cm") else w[b:b + 1] if k == "S0" else w) for k, w in v.items()}
+        n = at[b + 1] - at[b]
+        ry, rS, my, mS, _ = R.ssm(part["x"], part["dt"], v["A"], part["Bm"], part["Cm"], v["D"], v["dt_bias"], True,
+                                  part["S0"], _cu([n]))
+        ty, tS = _ssm_tol(ry, rS, my, mS, n, dtype, 64)
+        if n:
+            _close(y[one], ry, ty, f"sequence {b} y")
+        _close(S[b:b + 1], rS, tS, f"sequence {b} S")
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("lens", [[1] * 9, [2, 0, 1, 3], [16], [1, 0, 30, 0, 0, 0] * 3])
+def test_ssm_token_by_token_prompts(dtype, lens):
+    """Prompts short enough to run token by token, and just longer ones."""
+    _gpu()
+    cu = _cu(lens)
+    v = _ssm_inputs(19, (int(cu[-1]),), len(lens), 3, 1, 128, 64, dtype)
+    _check_ssm(v, cu, f"ssm short {ids(dtype)} {lens[:4]}")
+
+
+def test_ssm_growing_states():
+    """A rate above 0 makes the state grow: factors above 1 in every path."""
+    _gpu()
+    for dtype in (F32, BF16):
+        v = _ssm_inputs(23, (150,), 1, 2, 1, 64, 64, dtype)
+        v["A"] = torch.tensor([0.5, -2.0], device="cuda")
+        _check_ssm(v, _cu([150]), f"ssm growing {ids(dtype)}")
+
+
+def test_rows_beyond_32_bit_offsets():
+    """Rows of a projection so wide that element offsets pass 2^31 (4.3 GB)."""
+    _gpu()
+    g = _gen(41)
+    rows, ld = 70000, 32768
+    wide = torch.zeros((rows, ld), dtype=BF16, device="cuda")
+    at = rows - 200
+    C = 2 * 64 + 2 * 64
+    cols = _randn(g, (200, C + 2), BF16)
+    wide[at:, :C + 2] = cols
+    cu = torch.tensor([at, rows - 50, rows], dtype=torch.int32, device="cuda")
+    w = _randn(g, (C, 4))
+    y = lq.lq_conv_prefill(wide[:, :C], w, y=wide[:, 512:512 + C], cu=cu)[0]
+    local = torch.tensor([0, 150, 200], dtype=torch.int32, device="cuda")
+    want = lq.lq_conv_prefill(cols[:, :C].contiguous(), w, cu=local)[0]
+    assert torch.equal(y[at:], want) and (y[:at] == 0).all()
+    heads = lambda t: (t[:, :128].unflatten(-1, (2, 64)), t[:, 128:192].unflatten(-1, (1, 64)),   # noqa: E731
+                       t[:, 192:256].unflatten(-1, (1, 64)))
+    A = torch.tensor([-1.0, -4.0], device="cuda")
+    x, Bm, Cm = heads(y)
+    out = wide[:, 1024:1152].unflatten(-1, (2, 64))
+    _, S = lq.lq_ssm_prefill(x, wide[:, C:C + 2], A, Bm, Cm, y=out, cu=cu)
+    x, Bm, Cm = heads(want)
+    yl, Sl = lq.lq_ssm_prefill(x, cols[:, C:].contiguous(), A, Bm, Cm, cu=local)
+    for got, ref in ((out[at:], yl), (S, Sl)):
+        assert (got.double() - ref.double()).norm() <= 1e-2 * ref.double().norm()
+    wn = torch.ones(128, device="cuda")
+    n = lq.lq_norm_out(out.flatten(1)[:, None], wn, y=wide[:, 2048:2176].unflatten(-1, (1, 128)))
+    assert torch.equal(n[at:], lq.lq_norm_out(out[at:].reshape(200, 1, 128), wn))
+
+
 # -- norms --------------------------------------------------------------------------
 
 def _norm_tol(y, terms, dtype, D, act):

@@ -94,6 +94,20 @@ def test_ssm_prefill_refuses(cfg, kw, code):
     assert ssm(False, cfg, **kw) == code
 
 
+def test_ssm_workspace_is_checked():
+    """One long prompt of few heads needs a workspace: missing, misaligned, too
+    small or over another array it is refused."""
+    c = lq.lq_ssm_config(lq.LQ_BF16, 1, 4, 2, 128, 64, 1)
+    need = lq.lib().lq_ssm_workspace_bytes(C.addressof(c), 5000)
+    assert need > 0 and need % 256 == 0
+    one = {"B": 1}
+    assert ssm(False, one, rows=5000) == lq.LQ_ERR_WORKSPACE
+    assert ssm(False, one, rows=5000, ws=at(8, 16), n=need) == lq.LQ_ERR_WORKSPACE
+    assert ssm(False, one, rows=5000, ws=at(8), n=need - 1) == lq.LQ_ERR_WORKSPACE
+    assert ssm(False, one, rows=5000, ws=at(7), n=need) == lq.LQ_ERR_INVALID_ARG
+    assert lq.lq_ssm_workspace_bytes(torch.bfloat16, 1, 4, 2, 128, 64, 5000) == need
+
+
 def norm(inn, cfg=None, **kw):
     cfg = dict(dict(dtype=lq.LQ_BF16, x_dtype=lq.LQ_BF16, rows=5, G=1, D=64, w_groups=0, act=1, gate_first=0,
                     eps=1e-5, scale=1.0), **(cfg or {}))
