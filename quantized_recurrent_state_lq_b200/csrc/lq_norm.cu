@@ -55,6 +55,7 @@ __device__ __forceinline__ float team_sum(float v) {
 
 template <typename T, typename TX, int V, int TEAM, int NV, bool IN>
 __global__ void __launch_bounds__(TEAM > 128 ? TEAM : 128) norm_kernel(NormArgs a) {
+    static_assert(TEAM <= 32 || TEAM >= 128, "a team is part of a warp, or the CTA");
     constexpr int kTeams = (TEAM > 128 ? TEAM : 128) / TEAM;
     constexpr bool EXACT = sizeof(T) == 4;
     const int tid = threadIdx.x % TEAM;
@@ -148,6 +149,11 @@ cudaError_t launch(const NormArgs &a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+// Team and elements per thread by the group's size alone: few enough threads
+// that most of them have work, few enough elements (2 to 8 accesses in flight,
+// up to 64 elements in registers) that small groups do not step through empty
+// ones -- one class of 32 x 16 for all unaligned groups up to 512 took 96 us for
+// 8192 x 16 groups of 47.
 template <typename T, typename TX, bool IN>
 cudaError_t by_size(const NormArgs &a, cudaStream_t s) {
     const uintptr_t base = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.z) |
@@ -157,14 +163,20 @@ cudaError_t by_size(const NormArgs &a, cudaStream_t s) {
     const int u = 16 / (int)sizeof(T), ux = 16 / (int)sizeof(TX);
     if (a.D % 8 == 0 && base % 16 == 0 && a.ldx % ux == 0 && a.ldz % u == 0 && a.ldres % u == 0 && a.ldh % u == 0 &&
         a.ldy % u == 0) {
+        if (a.D <= 64) return launch<T, TX, 8, 8, 1, IN>(a, s);
         if (a.D <= 128) return launch<T, TX, 8, 16, 1, IN>(a, s);
         if (a.D <= 512) return launch<T, TX, 8, 32, 2, IN>(a, s);
         if (a.D <= 2048) return launch<T, TX, 8, 128, 2, IN>(a, s);
         if (a.D <= 4096) return launch<T, TX, 8, 256, 2, IN>(a, s);
         return launch<T, TX, 8, 512, 4, IN>(a, s);
     }
-    if (a.D <= 512) return launch<T, TX, 1, 32, 16, IN>(a, s);
-    if (a.D <= 4096) return launch<T, TX, 1, 256, 16, IN>(a, s);
+    if (a.D <= 16) return launch<T, TX, 1, 8, 2, IN>(a, s);
+    if (a.D <= 64) return launch<T, TX, 1, 32, 2, IN>(a, s);
+    if (a.D <= 128) return launch<T, TX, 1, 32, 4, IN>(a, s);
+    if (a.D <= 256) return launch<T, TX, 1, 128, 2, IN>(a, s);
+    if (a.D <= 512) return launch<T, TX, 1, 128, 4, IN>(a, s);
+    if (a.D <= 1024) return launch<T, TX, 1, 128, 8, IN>(a, s);
+    if (a.D <= 4096) return launch<T, TX, 1, 512, 8, IN>(a, s);
     return launch<T, TX, 1, 1024, 16, IN>(a, s);
 }
 
