@@ -10,7 +10,7 @@
 //   Y^T = 2^(g_t) (S^T C^T) + X^T M^T + D X^T
 //   S^T <- 2^(g_Q) S^T + X'^T B,  X'[s] = 2^(g_Q - g_s) d_s X[s]
 // f16 operands are exact in TF32; S, M and X' (and f32 operands) enter as two
-// TF32 parts, big x big + big x small + small x big: about 2^-21 of a term.
+// TF32 parts, big x big + big x small + small x big: about 2^-22 of a term.
 // Bound: latency of the MMA chains and the barriers between them, two to four
 // CTAs per SM.
 #include "lq_ssm.h"
@@ -27,29 +27,39 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// x = big + small: big is x cut to TF32 (a NaN or infinity stays one), small
-// the rest rounded to TF32 (within 2^-21 of x; whatever it is beside a big that
-// is not finite).
+// x = big + small, both rounded to TF32 (nearest, by adding half a unit to the
+// bits): within 2^-22 of x.  A NaN stays one in big (the addition would carry it
+// into the sign), an infinity too; small is whatever it is beside those.
 __device__ __forceinline__ void split(float x, uint32_t &big, uint32_t &small) {
-    big = __float_as_uint(x) & 0xffffe000u;
+    const uint32_t u = __float_as_uint(x);
+    big = x == x ? (u + 0x1000u) & 0xffffe000u : u;
     small = (__float_as_uint(x - __uint_as_float(big)) + 0x1000u) & 0xffffe000u;
 }
 
-// c += A B with A in two parts and B in PB parts (1: exact in TF32).
-template <int PB>
-__device__ __forceinline__ void mma_parts(float (&c)[4], const uint32_t (&ab)[4], const uint32_t (&as)[4], float b0,
+// c += A B with A in two parts and B exact in TF32.
+__device__ __forceinline__ void mma_exact(float (&c)[4], const uint32_t (&ab)[4], const uint32_t (&as)[4], float b0,
                                           float b1) {
-    if constexpr (PB == 1) {
-        mma_tf32(c, as, __float_as_uint(b0), __float_as_uint(b1));
-        mma_tf32(c, ab, __float_as_uint(b0), __float_as_uint(b1));
-    } else {
-        uint32_t bb[2], bs[2];
-        split(b0, bb[0], bs[0]);
-        split(b1, bb[1], bs[1]);
-        mma_tf32(c, as, bb[0], bb[1]);
-        mma_tf32(c, ab, bs[0], bs[1]);
-        mma_tf32(c, ab, bb[0], bb[1]);
-    }
+    mma_tf32(c, as, __float_as_uint(b0), __float_as_uint(b1));
+    mma_tf32(c, ab, __float_as_uint(b0), __float_as_uint(b1));
+}
+
+// A B with both in two parts: the products of the big parts into c, the others
+// (2^-11 of them) into d.  The tensor core's accumulation does not round to
+// nearest, so f32 results keep their chains of large terms short: apart from the
+// small ones, from the running state and (even and odd steps) from each other.
+__device__ __forceinline__ void mma_split(float (&c)[4], float (&d)[4], const uint32_t (&ab)[4], const uint32_t (&as)[4],
+                                          float b0, float b1) {
+    uint32_t bb[2], bs[2];
+    split(b0, bb[0], bs[0]);
+    split(b1, bb[1], bs[1]);
+    mma_tf32(d, as, bb[0], bb[1]);
+    mma_tf32(d, ab, bs[0], bs[1]);
+    mma_tf32(c, ab, bb[0], bb[1]);
+}
+
+__device__ __forceinline__ void split4(const float (&v)[4], uint32_t (&big)[4], uint32_t (&small)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split(v[e], big[e], small[e]);
 }
 
 template <int DK, int DV>
@@ -161,7 +171,7 @@ __global__ void __launch_bounds__(2 * DV, DV == 128 ? 2 : 4) ssm_tc_kernel(SsmAr
             // lower 16 x 8 tiles of G, one at a time per warp
             for (int tile = warp; tile < 6; tile += NW) {
                 const int rb = tile < 2 ? 0 : 16, cb = tile < 2 ? 8 * tile : 8 * (tile - 2);
-                float acc[2][4] = {};   // two chains
+                float acc[2][4] = {}, low[4] = {};   // two chains
 #pragma unroll 4
                 for (int k = 0; k < DK; k += 8) {
                     const float2 c0 = *reinterpret_cast<const float2 *>(&s.C[rb + gq][k + 2 * tq]);
@@ -174,34 +184,41 @@ __global__ void __launch_bounds__(2 * DV, DV == 128 ? 2 : 4) ssm_tc_kernel(SsmAr
                         mma_tf32(c, ar, __float_as_uint(b.x), __float_as_uint(b.y));
                     } else {
                         uint32_t ab[4], as[4];
-                        split(c0.x, ab[0], as[0]);
-                        split(c1.x, ab[1], as[1]);
-                        split(c0.y, ab[2], as[2]);
-                        split(c1.y, ab[3], as[3]);
-                        mma_parts<2>(c, ab, as, b.x, b.y);
+                        const float av[4] = {c0.x, c1.x, c0.y, c1.y};
+                        split4(av, ab, as);
+                        mma_split(c, low, ab, as, b.x, b.y);
                     }
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int t = rb + gq + (e >> 1) * 8, u = cb + 2 * tq + (e & 1);
-                    s.M[t][u] = u <= t ? exp2f(decay_f(s.g[t] - s.g[u])) * s.d[u] * (acc[0][e] + acc[1][e]) : 0.0f;
+                    s.M[t][u] = u <= t ? exp2f(decay_f(s.g[t] - s.g[u])) * s.d[u] * (acc[0][e] + acc[1][e] + low[e]) : 0.0f;
                 }
             }
         }
         float Y[Q / 8][4] = {};   // Y^T tile j: value columns pc + gq (+8), tokens 8 j + 2 tq (+1)
         if (FULL) {
+            constexpr int JS = PB == 1 ? Q / 8 : 2;   // token blocks at a time
 #pragma unroll
-            for (int i = 0; i < DK / 8; ++i) {
-                uint32_t ab[4], as[4];
-                split(S[i][0], ab[0], as[0]);
-                split(S[i][2], ab[1], as[1]);
-                split(S[i][1], ab[2], as[2]);
-                split(S[i][3], ab[3], as[3]);
+            for (int jb = 0; jb < Q / 8; jb += JS) {
+                float odd[JS][4] = {}, low[JS][4] = {};
 #pragma unroll
-                for (int j = 0; j < Q / 8; ++j) {
-                    const float2 c = *reinterpret_cast<const float2 *>(&s.C[8 * j + gq][8 * i + 2 * tq]);
-                    mma_parts<PB>(Y[j], ab, as, c.x, c.y);
+                for (int i = 0; i < DK / 8; ++i) {
+                    uint32_t ab[4], as[4];
+                    const float sv[4] = {S[i][0], S[i][2], S[i][1], S[i][3]};
+                    split4(sv, ab, as);
+#pragma unroll
+                    for (int j = 0; j < JS; ++j) {
+                        const float2 c = *reinterpret_cast<const float2 *>(&s.C[8 * (jb + j) + gq][8 * i + 2 * tq]);
+                        if constexpr (PB == 1) mma_exact(Y[jb + j], ab, as, c.x, c.y);
+                        else mma_split(i & 1 ? odd[j] : Y[jb + j], low[j], ab, as, c.x, c.y);
+                    }
                 }
+                if constexpr (PB == 2)
+#pragma unroll
+                    for (int j = 0; j < JS; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) Y[jb + j][e] += odd[j][e] + low[j][e];
             }
 #pragma unroll
             for (int j = 0; j < Q / 8; ++j) {
@@ -211,20 +228,25 @@ __global__ void __launch_bounds__(2 * DV, DV == 128 ? 2 : 4) ssm_tc_kernel(SsmAr
         }
         __syncthreads();   // M, and X without its non-finite values
         const float keep = s.keep;
+        auto x_at = [&](int u, float (&x)[4]) {
+            x[0] = s.X[u][pc + gq];
+            x[1] = s.X[u][pc + gq + 8];
+            x[2] = s.X[u + 1][pc + gq];
+            x[3] = s.X[u + 1][pc + gq + 8];
+        };
+        if constexpr (PB == 1) {
 #pragma unroll
-        for (int i = 0; i < DK / 8; ++i)
+            for (int i = 0; i < DK / 8; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) S[i][e] *= keep;
+                for (int e = 0; e < 4; ++e) S[i][e] *= keep;
 #pragma unroll
-        for (int k = 0; k < Q / 8; ++k) {   // 8 tokens
-            const int u = 8 * k + 2 * tq;
-            const float x0 = s.X[u][pc + gq], x1 = s.X[u][pc + gq + 8];
-            const float x2 = s.X[u + 1][pc + gq], x3 = s.X[u + 1][pc + gq + 8];
-            uint32_t ab[4], as[4];
-            if (FULL) {
-                if constexpr (PB == 1) {
-                    const uint32_t ar[4] = {__float_as_uint(x0), __float_as_uint(x1), __float_as_uint(x2),
-                                            __float_as_uint(x3)};
+            for (int k = 0; k < Q / 8; ++k) {   // 8 tokens
+                const int u = 8 * k + 2 * tq;
+                float x[4];
+                x_at(u, x);
+                if (FULL) {
+                    const uint32_t ar[4] = {__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                                            __float_as_uint(x[3])};
 #pragma unroll
                     for (int j = k; j < Q / 8; ++j) {
                         const float2 m = *reinterpret_cast<const float2 *>(&s.M[8 * j + gq][u]);
@@ -234,26 +256,56 @@ __global__ void __launch_bounds__(2 * DV, DV == 128 ? 2 : 4) ssm_tc_kernel(SsmAr
                         mma_tf32(Y[j], ar, ms[0], ms[1]);
                         mma_tf32(Y[j], ar, mb[0], mb[1]);
                     }
-                } else {
-                    split(x0, ab[0], as[0]);
-                    split(x1, ab[1], as[1]);
-                    split(x2, ab[2], as[2]);
-                    split(x3, ab[3], as[3]);
+                }
+                const float w0 = s.w[u], w1 = s.w[u + 1];
+                const float xw[4] = {x[0] * w0, x[1] * w0, x[2] * w1, x[3] * w1};
+                uint32_t ab[4], as[4];
+                split4(xw, ab, as);
 #pragma unroll
-                    for (int j = k; j < Q / 8; ++j) {
+                for (int i = 0; i < DK / 8; ++i) mma_exact(S[i], ab, as, s.B[u][8 * i + gq], s.B[u + 1][8 * i + gq]);
+            }
+        } else {
+            if (FULL)
+#pragma unroll
+                for (int j = 0; j < Q / 8; ++j) {
+                    float acc[4] = {}, low[4] = {};
+#pragma unroll
+                    for (int k = 0; k <= j; ++k) {
+                        const int u = 8 * k + 2 * tq;
+                        float x[4];
+                        x_at(u, x);
+                        uint32_t ab[4], as[4];
+                        split4(x, ab, as);
                         const float2 m = *reinterpret_cast<const float2 *>(&s.M[8 * j + gq][u]);
-                        mma_parts<2>(Y[j], ab, as, m.x, m.y);
+                        mma_split(acc, low, ab, as, m.x, m.y);
                     }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) Y[j][e] += acc[e] + low[e];
+                }
+#pragma unroll
+            for (int kb = 0; kb < Q / 8; kb += 2) {   // 16 tokens
+                uint32_t ab[2][4], as[2][4];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int u = 8 * (kb + k) + 2 * tq;
+                    float x[4];
+                    x_at(u, x);
+                    const float w0 = s.w[u], w1 = s.w[u + 1];
+                    const float xw[4] = {x[0] * w0, x[1] * w0, x[2] * w1, x[3] * w1};
+                    split4(xw, ab[k], as[k]);
+                }
+#pragma unroll
+                for (int i = 0; i < DK / 8; ++i) {
+                    float acc[4] = {}, low[4] = {};
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int u = 8 * (kb + k) + 2 * tq;
+                        mma_split(acc, low, ab[k], as[k], s.B[u][8 * i + gq], s.B[u + 1][8 * i + gq]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) S[i][e] = fmaf(kb == 0 ? keep : 1.0f, S[i][e], acc[e] + low[e]);
                 }
             }
-            const float w0 = s.w[u], w1 = s.w[u + 1];
-            split(x0 * w0, ab[0], as[0]);
-            split(x1 * w0, ab[1], as[1]);
-            split(x2 * w1, ab[2], as[2]);
-            split(x3 * w1, ab[3], as[3]);
-#pragma unroll
-            for (int i = 0; i < DK / 8; ++i)
-                mma_parts<PB>(S[i], ab, as, s.B[u][8 * i + gq], s.B[u + 1][8 * i + gq]);
         }
         // from a non-finite x on, its column has no finite state
         const int f0 = s.first[pc + gq], f1 = s.first[pc + gq + 8];
