@@ -353,7 +353,7 @@ int lq_damp_select(const lq_config *cfg, int32_t n_states, const float *d_states
  * width keep 16-byte alignment take vector accesses; others give the same
  * results up to rounding order, at a lower rate.
  *
- * Prompts: `rows` token rows in all, of B sequences.
+ * Prompts: `rows` token rows in all (at most 2^30), of B sequences.
  *   d_cu NULL:  equal lengths T = rows / B (rows divisible by B, else
  *               LQ_ERR_SHAPE), time-major as in lq_prefill: token t of sequence
  *               b is row t*B + b.
@@ -419,13 +419,19 @@ size_t lq_ssm_workspace_bytes(const lq_ssm_config *cfg, int32_t rows);
  *   decaying state), d_D [H] or NULL (0), d_dt_bias [H] or NULL (0)
  *   -> d_y [rows,H,dv] and the final states d_S_out [B,H,dk,dv], from d_S0 [B,H,dk,dv]
  *   (NULL = zeros; d_S_out may be d_S0).
- * Long prompts run in chunks whose products use the tensor cores with FP32-level
- * accuracy; one step's log decay d_t A_h is floored at -104 there (2^-150: a
- * factor that FP32 flushes to 0).  d_ws: caller-owned device workspace of at
- * least lq_ssm_workspace_bytes(cfg, rows) bytes, 256-byte aligned (else
- * LQ_ERR_WORKSPACE; NULL when that is 0), used by this call until it completes
- * on `stream`: calls that may overlap need a workspace each, graphs that may
- * run at the same time included.  d_y must not overlap an input.
+ * Prompts of more than a few tokens run in chunks whose products use the tensor
+ * cores: the state with FP32-level accuracy, the outputs within 2^-17 of their
+ * terms for bf16 (two-part operands; one rounding to bf16 is 2^-9) and FP32-level
+ * for f32 and f16.  One step's decay exp(d_t A_h) is kept within 2^-150 .. 2^150
+ * there (beyond, FP32 has 0 and infinity).  A value of x, Bm, Cm or dt that is not
+ * finite shows in the outputs and states it reaches and in no earlier token; where
+ * it reaches a state's column or row, those entries are not finite (NaN or
+ * infinite).  A call gives the same bits every time.
+ * d_ws: caller-owned device workspace of at least lq_ssm_workspace_bytes(cfg, rows)
+ * bytes, 256-byte aligned (else LQ_ERR_WORKSPACE; NULL when that is 0), used by
+ * this call until it completes on `stream`: calls that may overlap need a
+ * workspace each, graphs that may run at the same time included.  d_y must not
+ * overlap an input.
  */
 int lq_ssm_prefill(const lq_ssm_config *cfg, int32_t rows, const int32_t *d_cu, const void *d_x, int64_t ldx,
                    const void *d_dt, int64_t lddt, const float *d_A, const void *d_Bm, int64_t ldb, const void *d_Cm,

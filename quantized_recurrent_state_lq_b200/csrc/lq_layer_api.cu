@@ -50,7 +50,7 @@ bool bad_ld(int64_t ld, int64_t width) { return ld < width || ld > (1ll << 28); 
 // The rows of a prompt batch.
 int check_rows(int32_t B, int32_t rows, const int32_t *d_cu) {
     if (B < 1) return LQ_ERR_SHAPE;
-    if (rows < 0 || misaligned(d_cu, 4)) return LQ_ERR_INVALID_ARG;
+    if (rows < 0 || rows > (1 << 30) || misaligned(d_cu, 4)) return LQ_ERR_INVALID_ARG;
     if (!d_cu && rows % B != 0) return LQ_ERR_SHAPE;
     return LQ_OK;
 }

