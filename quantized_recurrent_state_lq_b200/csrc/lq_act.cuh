@@ -229,6 +229,15 @@ __device__ __forceinline__ int last_sequence(const Rows &r, int seg, int add, in
     return lo;
 }
 
+// Sequence b's pieces, and the first of them.
+__device__ __forceinline__ int pieces_of(const Rows &r, int seg, int b) {
+    const int len = r.cu ? cu_at(r, b + 1) - cu_at(r, b) : r.rows / r.B;
+    return len > seg ? (len + seg - 1) / seg : 1;
+}
+__device__ __forceinline__ int64_t first_piece(const Rows &r, int seg, int b) {
+    return r.cu ? cu_at(r, b) / seg + b : (int64_t)b * pieces_of(r, seg, b);
+}
+
 // (Called by whole warps, every lane with the same id.)
 __device__ __forceinline__ bool find_piece(const Rows &r, int seg, int id, Piece &p) {
     p.id = id;

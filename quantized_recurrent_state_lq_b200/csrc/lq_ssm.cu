@@ -122,57 +122,80 @@ cudaError_t launch_ssm_step(const SsmArgs &a, int dtype, cudaStream_t s) {
 
 namespace {
 
-// One thread per 4 state elements of a sequence; blockIdx.y counts the places
-// where a sequence may be cut, its first one does the work.
-__global__ void __launch_bounds__(256) ssm_join_kernel(SsmArgs a, int seg, int cuts) {
+constexpr int kJoin = 8, kJoinThreads = 128;
+
+// One thread per 4 state elements; block y takes every gridDim.y-th sequence and
+// skips those of one piece, 32 at a time.  kJoin pieces' states are on their way
+// at a time (128 pieces of 2 heads of 64 x 64: 37 us for the prompt, 62 one by one).
+__global__ void __launch_bounds__(kJoinThreads) ssm_join_kernel(SsmArgs a, int seg) {
     const int64_t per = (int64_t)a.dk * a.dv / 4, all = per * a.H;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;   // (head, element)
-    for (int k = blockIdx.y; k < cuts; k += gridDim.y) {
-        Piece p;
-        if (!find_cut(a.r, seg, k, p) || p.j != 0 || i >= all) continue;
-        const float *decay = ssm_decays(a, seg) + p.id * a.H + i / per;
-        float4 *slot = reinterpret_cast<float4 *>(a.ws) + p.id * all + i;
-        float4 S = a.S0 ? reinterpret_cast<const float4 *>(a.S0)[p.b * all + i] : make_float4(0.f, 0.f, 0.f, 0.f);
-        float4 own = slot[0];
-        for (int j = 0; j < p.n; ++j) {
-            float4 *at = slot + j * all;
-            float4 next = own;
-            if (j + 2 < p.n) next = at[all];   // the last piece has no state of its own
-            *at = S;
-            if (j + 1 < p.n) {
-                const float f = decay[(int64_t)j * a.H];
-                S = make_float4(fmaf(f, S.x, own.x), fmaf(f, S.y, own.y), fmaf(f, S.z, own.z), fmaf(f, S.w, own.w));
+    const int64_t i = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x;   // (head, element)
+    const int lane = threadIdx.x & 31, step = gridDim.y;
+    for (int64_t b0 = blockIdx.y; b0 < a.r.B; b0 += 32 * step) {
+        const int64_t bl = b0 + lane * step;
+        unsigned todo = __ballot_sync(0xffffffffu, bl < a.r.B && pieces_of(a.r, seg, (int)bl) > 1);
+        for (; todo; todo &= todo - 1) {
+            const int b = (int)(b0 + (__ffs(todo) - 1) * step), n = pieces_of(a.r, seg, b);
+            if (i >= all) continue;
+            const int64_t id = first_piece(a.r, seg, b);
+            const float *decay = ssm_decays(a, seg) + id * a.H + i / per;
+            float4 *slot = reinterpret_cast<float4 *>(a.ws) + id * all + i;
+            float4 S = a.S0 ? reinterpret_cast<const float4 *>(a.S0)[b * all + i] : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int j0 = 0; j0 < n; j0 += kJoin) {
+                float4 own[kJoin];
+                float f[kJoin];
+#pragma unroll
+                for (int j = 0; j < kJoin; ++j)
+                    if (j0 + j + 1 < n) {   // the last piece has no state of its own
+                        own[j] = slot[j * all];
+                        f[j] = decay[j * a.H];
+                    }
+#pragma unroll
+                for (int j = 0; j < kJoin; ++j) {
+                    if (j0 + j < n) slot[j * all] = S;
+                    if (j0 + j + 1 < n)
+                        S = make_float4(fmaf(f[j], S.x, own[j].x), fmaf(f[j], S.y, own[j].y),
+                                        fmaf(f[j], S.z, own[j].z), fmaf(f[j], S.w, own[j].w));
+                }
+                slot += kJoin * all;
+                decay += (int64_t)kJoin * a.H;
             }
-            own = next;
         }
     }
 }
 
 // Tokens per piece: pieces are cut so that the batch gives about as many CTAs
 // as the GPU runs side by side -- for bf16 one per SM and 128 value columns, else
-// two per SM and a head each.  A batch with enough sequences and heads is cut
-// only where a sequence is longer than a CTA's share of all tokens.
+// a head each, two per SM for 128 value columns and four for 64 (16384 tokens of 16
+// heads of 64 x 64: 273 us against 407 with two).  A batch with enough sequences
+// and heads is cut only where a sequence is longer than a CTA's share of all
+// tokens.  Pieces hold whole chunks, down to a single one.
 int piece_tokens(const Rows &r, int dtype, int H, int G, int dv) {
-    int64_t units = H, slots = 148 * 2;
+    int64_t units = H, slots = dv == 64 ? 148 * 4 : 148 * 2, chunk = 32;
     if (dtype == kBF16) {
         slots = 148;
+        chunk = 128;
         if (dv == 64) units = (int64_t)G * ((H / G + 1) / 2);
     }
     const int64_t share = units <= slots ? (r.rows + slots / units - 1) / (slots / units)
                                          : (r.rows * units + slots - 1) / slots;
-    const int64_t seg = (share + 127) / 128 * 128;
-    return (int)(seg < 128 ? 128 : seg > (1 << 30) ? (1 << 30) : seg);
+    const int64_t seg = (share + chunk - 1) / chunk * chunk;
+    return (int)(seg < chunk ? chunk : seg > (1 << 30) ? (1 << 30) : seg);
 }
 
-// Whether a sequence can be longer than a piece.
-bool may_split(const Rows &r, int seg) { return (r.cu ? r.rows : r.rows / r.B) > seg; }
+// Sequences of at most this length are not cut: the two launches more cost what
+// four chunks of 32 do.
+constexpr int kWhole = 128;
+
+// The longest that a sequence can be.
+int64_t longest(const Rows &r) { return r.cu ? r.rows : r.rows / r.B; }
 
 }  // namespace
 
 cudaError_t launch_ssm_join(const SsmArgs &a, int seg, cudaStream_t s) {
-    const int64_t n = (int64_t)a.H * a.dk * a.dv / 4, cuts = cut_count(a.r, seg);
-    ssm_join_kernel<<<dim3((unsigned)((n + 255) / 256), (unsigned)(cuts < 65535 ? cuts : 65535)), 256, 0, s>>>(
-        a, seg, (int)cuts);
+    const int64_t n = (int64_t)a.H * a.dk * a.dv / 4, x = (n + kJoinThreads - 1) / kJoinThreads;
+    const int64_t y = (4 * 148 + x - 1) / x;   // about four CTAs per SM
+    ssm_join_kernel<<<dim3((unsigned)x, (unsigned)(y < a.r.B ? y : a.r.B)), kJoinThreads, 0, s>>>(a, seg);
     return cudaGetLastError();
 }
 
@@ -189,16 +212,17 @@ bool token_by_token(const Rows &r) {
 size_t ssm_ws_bytes(int dtype, int B, int rows, int H, int G, int dk, int dv) {
     Rows r{nullptr, B, rows};
     const int seg = piece_tokens(r, dtype, H, G, dv);
-    if (rows <= seg) return 0;
+    if (rows <= seg || rows <= kWhole) return 0;
     // packed: at most rows / seg + B pieces, no fewer than time-major ones
     return ((size_t)(rows / seg + B) * H * (dk * dv + 1) * 4 + 255) / 256 * 256;
 }
 
 cudaError_t launch_ssm_prefill(const SsmArgs &a, int dtype, cudaStream_t s) {
     if (token_by_token(a.r)) return launch_ssm_step(a, dtype, s);
-    const int seg = piece_tokens(a.r, dtype, a.H, a.G, a.dv);
-    if (dtype == kBF16) return launch_ssm_umma(a, seg, may_split(a.r, seg), s);
-    return launch_ssm_tc(a, dtype, seg, may_split(a.r, seg), s);
+    const int seg = longest(a.r) <= kWhole ? kWhole : piece_tokens(a.r, dtype, a.H, a.G, a.dv);
+    const bool cut = longest(a.r) > seg;
+    if (dtype == kBF16) return launch_ssm_umma(a, seg, cut, s);
+    return launch_ssm_tc(a, dtype, seg, cut, s);
 }
 
 }  // namespace lq

@@ -46,8 +46,8 @@ __device__ __forceinline__ long long warp_scan(long long v) {
 // piece, slot <- S and S <- decay S + own.
 cudaError_t launch_ssm_join(const SsmArgs &a, int seg, cudaStream_t s);
 
-// The chunked scans, with pieces of seg tokens (a multiple of 128); split: at
-// least one sequence may be cut.
+// The chunked scans, with pieces of seg tokens (whole chunks); split: at least
+// one sequence may be cut.
 cudaError_t launch_ssm_umma(const SsmArgs &a, int seg, bool split, cudaStream_t s);            // bf16
 cudaError_t launch_ssm_tc(const SsmArgs &a, int dtype, int seg, bool split, cudaStream_t s);   // f32, f16
 

@@ -225,6 +225,18 @@ def test_ssm_long_sequence():
         _check_ssm(v, cu, f"ssm long {ids(dtype)}")
 
 
+def test_ssm_few_long_among_many_sequences():
+    """Three of 70 sequences are split along their length, behind and between
+    short and empty ones (heads enough that one pass looks over 32 or 64)."""
+    _gpu()
+    for dtype in (F32, BF16):
+        lens = [7 * i % 23 for i in range(70)]
+        lens[1], lens[66], lens[69] = 700, 1100, 300
+        cu = _cu(lens)
+        v = _ssm_inputs(8, (int(cu[-1]),), 70, 16, 1, 128, 128, dtype)
+        _check_ssm(v, cu, f"ssm few long {ids(dtype)}")
+
+
 def test_ssm_extreme_steps():
     """Steps of 0, of 1e-30 and so large that a token wipes the state: no
     inf - inf inside a chunk, and what follows depends on the wiping token on."""
