@@ -1,13 +1,15 @@
 """Build liblq.so (the CUDA library behind include/lq_state.h) in-tree.
 
 nvcc compiles every csrc/*.cu for sm_100a only and links them, with the CUDA
-runtime linked statically, into quantized_recurrent_state_lq_b200/liblq.so.
+runtime linked statically, into quantized_recurrent_state_lq_b200/liblq.so;
+g++ compiles csrc/lq_bind.cpp (host code, against torch) into _bind.so beside it.
 Run `python -m quantized_recurrent_state_lq_b200.build` or call build().
 """
 from __future__ import annotations
 
 import glob
 import os
+import shutil
 import subprocess
 import sys
 
@@ -15,6 +17,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "liblq.so")
+BIND_SRC = os.path.join(CSRC, "lq_bind.cpp")
+BIND_OUT = os.path.join(HERE, "_bind.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -35,7 +39,39 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def bind_stale() -> bool:
+    if not os.path.exists(BIND_OUT):
+        return True
+    deps = [BIND_SRC, os.path.join(ROOT, "include", "lq_state.h")]
+    return any(os.path.getmtime(d) > os.path.getmtime(BIND_OUT) for d in deps)
+
+
+def _bind_command(out: str) -> list[str]:
+    import sysconfig
+
+    import torch
+    tdir = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(shutil.which(NVCC) or NVCC))
+    inc = [os.path.join(tdir, "include"), os.path.join(tdir, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include")]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + os.path.join(ROOT, "include"),
+            "-I" + sysconfig.get_paths()["include"], *(a for d in inc for a in ("-isystem", d)), BIND_SRC,
+            "-L" + os.path.join(tdir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-o", out]
+
+
+def build_bind(verbose: bool = False) -> str:
+    cmd = _bind_command(BIND_OUT + ".tmp")
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(BIND_OUT + ".tmp", BIND_OUT)
+    return BIND_OUT
+
+
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
+    if force or bind_stale():
+        build_bind(verbose)
     if not force and not _stale():
         return OUT
     objs = []

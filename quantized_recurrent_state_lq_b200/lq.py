@@ -2,13 +2,13 @@
 
 Argument marshalling only: torch tensors are checked for device, dtype, shape
 and contiguity and passed as raw device pointers together with torch's current
-CUDA stream.  Every computation happens in the CUDA library; if liblq.so is
-missing this module raises on import of the library instead of falling back.
+CUDA stream (for the recurrent layer's calls by csrc/lq_bind.cpp).  Every
+computation happens in the CUDA library; if liblq.so is missing this module
+raises on import of the library instead of falling back.
 """
 from __future__ import annotations
 
 import ctypes as C
-import functools
 import os
 from dataclasses import dataclass
 
@@ -80,6 +80,8 @@ def lib():
         from . import build as _build
         if not os.path.exists(LIB_PATH) or _build._stale():
             _build.build()
+        elif _build.bind_stale():
+            _build.build_bind()
         L = C.CDLL(LIB_PATH)
         vp, i32, i64, sz = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t
         cfgp = C.POINTER(lq_config)
@@ -441,7 +443,8 @@ def lq_state_destroy(st: LqState):
 # The recurrent layer around the state: short causal convolution, selective
 # state-space scan, norms.  Activations float32, bfloat16 or float16; prompts
 # are packed ([rows, ...] with cu, the B+1 int32 row offsets on the device) or
-# time-major ([T, B, ...]); rows may be columns of a wider tensor.
+# time-major ([T, B, ...]); rows may be columns of a wider tensor.  Calls run on
+# torch's current stream of their first argument's device, or on stream=.
 # ---------------------------------------------------------------------------
 LQ_F32, LQ_BF16, LQ_F16 = 0, 1, 2
 LQ_ACT_NONE, LQ_ACT_SILU, LQ_ACT_SIGMOID = 0, 1, 2
@@ -449,158 +452,61 @@ LQ_CONV_MAX_TAPS = 4
 LQ_NORM_MAX_D = 16384
 
 _DTYPES = {torch.float32: LQ_F32, torch.bfloat16: LQ_BF16, torch.float16: LQ_F16}
-_ACTS = {None: LQ_ACT_NONE, "silu": LQ_ACT_SILU, "sigmoid": LQ_ACT_SIGMOID}
+
+_BOUND = ("lq_conv_prefill", "lq_conv_step", "lq_ssm_workspace_bytes", "lq_ssm_prefill", "lq_ssm_step", "lq_norm_in",
+          "lq_norm_out")
+_native = None
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream    # the current stream's handle, without a Stream object
+def _binding():
+    """The native half of these calls (csrc/lq_bind.cpp), which checks the
+    tensors, allocates what is not given and calls liblq.so on torch's current
+    stream of the first argument's device."""
+    global _native
+    if _native is None:
+        L = lib()
+        from . import _bind
+        _bind.load(*(C.cast(getattr(L, n), C.c_void_p).value for n in _BOUND))
+        _native = _bind
+    return _native
 
 
-def _layer_call(fn):
-    """A call on the device of its first argument and on torch's current stream
-    of it, or on the given stream: both are made current for the call, so that
-    what it allocates belongs to the stream it is used on, and the arguments'
-    memory is not reused before that stream is done with it."""
-
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        t = args[0] if args else next(iter(kw.values()), None)
+def _call(name: str, args, stream):
+    """The call `name` of the binding, on the given stream if there is one: made
+    current for the call, so that what it allocates belongs to the stream it is
+    used on, and the arguments' memory is not reused before that stream is done
+    with it."""
+    fn = getattr(_binding(), name)
+    if stream is None:
+        out = fn(*args)
+    else:
+        t = args[0]
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError(f"{fn.__name__} takes CUDA tensors")
-        if stream is None:
-            if t.get_device() == torch._C._cuda_getDevice():
-                return fn(*args, **kw)
-            with torch.cuda.device(t.device):
-                return fn(*args, **kw)
+            raise TypeError(f"lq_{name} takes CUDA tensors")
         if stream.device != t.device:
             raise ValueError(f"stream of {stream.device} for tensors on {t.device}")
         with torch.cuda.stream(stream):
-            out = fn(*args, **kw)
-            for v in (*args, *kw.values()):
+            out = fn(*args)
+            for v in args:
                 if isinstance(v, torch.Tensor) and v.is_cuda:
                     v.record_stream(stream)
-            return out
-
-    return call
-
-
-def _refuse(t, name: str, shape, dtype, dev: int):
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
-        raise TypeError(f"{name} must be a CUDA tensor on device {dev}")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if out.__class__ is int:
+        raise LqError(out, f"lq_{name}")
+    return out
 
 
-def _rows(t, name: str, shape, n_tail: int, width: int, dtype, dev: int):
-    """Pointer and row stride of a tensor of token rows: its last n_tail
-    dimensions are one contiguous row of `width` elements, the others evenly
-    spaced rows."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
-        _refuse(t, name, shape, dtype, dev)
-    if t.is_contiguous():
-        return t.data_ptr(), width
-    st = t.stride()
-    n = len(st)
-    w = 1
-    for i in range(n - 1, n - 1 - n_tail, -1):
-        if shape[i] != 1:
-            if st[i] != w:
-                raise ValueError(f"{name}: the elements of a row must be contiguous")
-            w *= shape[i]
-    ld, rows = width, 1
-    for i in range(n - n_tail - 1, -1, -1):
-        if shape[i] != 1:
-            if rows == 1:
-                ld = st[i]
-            elif st[i] != rows * ld:
-                raise ValueError(f"{name}: rows must be evenly spaced")
-            rows *= shape[i]
-    return t.data_ptr(), ld
-
-
-def _flat(t, name: str, shape, dev: int, dtype=torch.float32):
-    """Pointer of an optional contiguous tensor."""
-    if t is None:
-        return None
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
-        _refuse(t, name, shape, dtype, dev)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _dtype_of(t: torch.Tensor) -> int:
-    if t.dtype not in _DTYPES:
-        raise TypeError(f"activations must be float32, bfloat16 or float16, got {t.dtype}")
-    return _DTYPES[t.dtype]
-
-
-def _act_of(act) -> int:
-    if act not in _ACTS:
-        raise ValueError(f"unknown activation {act!r}")
-    return _ACTS[act]
-
-
-def _prompt(x: torch.Tensor, cu, n_tail: int, dev: int):
-    """(B, rows, pointer of cu or None) of a packed or time-major prompt batch."""
-    lead = x.shape[:x.dim() - n_tail]
-    if cu is None:
-        if len(lead) != 2:
-            raise ValueError(f"a time-major prompt is [T, B, ...], got {tuple(x.shape)}; a packed one needs cu")
-        return lead[1], lead[0] * lead[1], None
-    if len(lead) != 1:
-        raise ValueError(f"a packed prompt is [rows, ...], got {tuple(x.shape)}")
-    if cu.dim() != 1 or cu.shape[0] < 2:
-        raise ValueError("cu must hold B+1 offsets")
-    return cu.shape[0] - 1, lead[0], _flat(cu, "cu", cu.shape, dev, torch.int32)
-
-
-def _scale(scale, shape, dev: int):
-    """(factor, pointer of the per-channel scale) of a number or a tensor."""
-    if isinstance(scale, torch.Tensor):
-        return 1.0, _flat(scale, "scale", shape, dev)
-    return float(scale), None
-
-
-@_layer_call
-def lq_conv_prefill(x, w, bias=None, act="silu", state0=None, state_out=None, y=None, cu=None):
+def lq_conv_prefill(x, w, bias=None, act="silu", state0=None, state_out=None, y=None, cu=None, stream=None):
     """Short causal depthwise convolution over prompts x ([rows, C] with cu, or
     [T, B, C]) with taps w [C, K], from the windows state0 [B, K-1, C] (None:
     zeros).  Returns (y, state_out), allocated when None; state_out may be
-    state0.  Takes stream=."""
-    dt, dev, code = x.dtype, x.get_device(), _dtype_of(x)
-    B, rows, p_cu = _prompt(x, cu, 1, dev)
-    ch, K = w.shape
-    shape = (*x.shape[:-1], ch)
-    px, ldx = _rows(x, "x", shape, 1, ch, dt, dev)
-    y = x.new_empty(shape) if y is None else y
-    py, ldy = _rows(y, "y", shape, 1, ch, dt, dev)
-    win = (B, K - 1, ch)
-    state_out = x.new_empty(win) if state_out is None else state_out
-    cfg = lq_conv_config(code, B, ch, K, _act_of(act))
-    rc = lib().lq_conv_prefill(C.addressof(cfg), rows, p_cu, px, ldx, _flat(w, "w", (ch, K), dev),
-                               _flat(bias, "bias", (ch,), dev), _flat(state0, "state0", win, dev, dt),
-                               _flat(state_out, "state_out", win, dev, dt), py, ldy, _raw_stream(dev))
-    _chk(rc, "lq_conv_prefill")
-    return y, state_out
+    state0."""
+    return _call("conv_prefill", (x, w, bias, act, state0, state_out, y, cu), stream)
 
 
-@_layer_call
-def lq_conv_step(state, x, w, bias=None, act="silu", y=None):
+def lq_conv_step(state, x, w, bias=None, act="silu", y=None, stream=None):
     """One token of every sequence, x [B, C]; the windows state [B, K-1, C] move
-    on in place.  Returns y [B, C] (allocated when None; may be x).  Takes
-    stream=."""
-    dt, dev, code = x.dtype, x.get_device(), _dtype_of(x)
-    ch, K = w.shape
-    B = x.shape[0]
-    px, ldx = _rows(x, "x", (B, ch), 1, ch, dt, dev)
-    y = x.new_empty((B, ch)) if y is None else y
-    py, ldy = _rows(y, "y", (B, ch), 1, ch, dt, dev)
-    cfg = lq_conv_config(code, B, ch, K, _act_of(act))
-    rc = lib().lq_conv_step(C.addressof(cfg), _flat(state, "state", (B, K - 1, ch), dev, dt), px, ldx,
-                            _flat(w, "w", (ch, K), dev), _flat(bias, "bias", (ch,), dev), py, ldy, _raw_stream(dev))
-    _chk(rc, "lq_conv_step")
-    return y
+    on in place.  Returns y [B, C] (allocated when None; may be x)."""
+    return _call("conv_step", (state, x, w, bias, act, y), stream)
 
 
 def lq_ssm_workspace_bytes(dtype, B: int, H: int, G: int, dk: int, dv: int, rows: int) -> int:
@@ -609,111 +515,34 @@ def lq_ssm_workspace_bytes(dtype, B: int, H: int, G: int, dk: int, dv: int, rows
     return lib().lq_ssm_workspace_bytes(C.addressof(cfg), rows)
 
 
-@_layer_call
 def lq_ssm_prefill(x, dt, A, Bm, Cm, D=None, dt_bias=None, softplus=True, S0=None, S_out=None, y=None, cu=None,
-                   workspace=None):
+                   workspace=None, stream=None):
     """Selective state-space scan over prompts: x [..., H, dv], dt [..., H],
     Bm, Cm [..., G, dk] with [...] = [rows] (and cu) or [T, B]; A, D, dt_bias
     [H].  From the states S0 [B, H, dk, dv] (None: zeros).  Returns
     (y [..., H, dv], S_out), allocated when None; S_out may be S0.  The
-    workspace (uint8, at least lq_ssm_workspace_bytes) is allocated when None.
-    Takes stream=."""
-    t, dev, code = x.dtype, x.get_device(), _dtype_of(x)
-    B, rows, p_cu = _prompt(x, cu, 2, dev)
-    lead, (H, dv), (G, dk) = x.shape[:-2], x.shape[-2:], Bm.shape[-2:]
-    sx, sb = (*lead, H, dv), (*lead, G, dk)
-    px, ldx = _rows(x, "x", sx, 2, H * dv, t, dev)
-    pd, ldd = _rows(dt, "dt", (*lead, H), 1, H, t, dev)
-    pb, ldb = _rows(Bm, "Bm", sb, 2, G * dk, t, dev)
-    pc, ldc = _rows(Cm, "Cm", sb, 2, G * dk, t, dev)
-    y = x.new_empty(sx) if y is None else y
-    py, ldy = _rows(y, "y", sx, 2, H * dv, t, dev)
-    st, hs = (B, H, dk, dv), (H,)
-    S_out = x.new_empty(st, dtype=torch.float32) if S_out is None else S_out
-    cfg = lq_ssm_config(code, B, H, G, dk, dv, 1 if softplus else 0)
-    L, p_cfg = lib(), C.addressof(cfg)
-    n_ws = L.lq_ssm_workspace_bytes(p_cfg, rows)
-    if workspace is None and n_ws:
-        workspace = x.new_empty(n_ws, dtype=torch.uint8)
-    p_ws = None
-    if workspace is not None:
-        n_ws = workspace.numel()
-        p_ws = _flat(workspace, "workspace", (n_ws,), dev, torch.uint8)
-    rc = L.lq_ssm_prefill(p_cfg, rows, p_cu, px, ldx, pd, ldd, _flat(A, "A", hs, dev), pb, ldb, pc, ldc,
-                          _flat(D, "D", hs, dev), _flat(dt_bias, "dt_bias", hs, dev), _flat(S0, "S0", st, dev),
-                          _flat(S_out, "S_out", st, dev), py, ldy, p_ws, n_ws, _raw_stream(dev))
-    _chk(rc, "lq_ssm_prefill")
-    return y, S_out
+    workspace (uint8, at least lq_ssm_workspace_bytes) is allocated when None."""
+    return _call("ssm_prefill", (x, dt, A, Bm, Cm, D, dt_bias, softplus, S0, S_out, y, cu, workspace), stream)
 
 
-@_layer_call
-def lq_ssm_step(S, x, dt, A, Bm, Cm, D=None, dt_bias=None, softplus=True, y=None):
+def lq_ssm_step(S, x, dt, A, Bm, Cm, D=None, dt_bias=None, softplus=True, y=None, stream=None):
     """One token of every sequence: x [B, H, dv], dt [B, H], Bm, Cm [B, G, dk];
     the states S [B, H, dk, dv] are updated in place.  Returns y [B, H, dv]
-    (allocated when None).  Takes stream=."""
-    t, dev, code = x.dtype, x.get_device(), _dtype_of(x)
-    (B, H, dv), (G, dk) = x.shape, Bm.shape[-2:]
-    px, ldx = _rows(x, "x", (B, H, dv), 2, H * dv, t, dev)
-    pd, ldd = _rows(dt, "dt", (B, H), 1, H, t, dev)
-    pb, ldb = _rows(Bm, "Bm", (B, G, dk), 2, G * dk, t, dev)
-    pc, ldc = _rows(Cm, "Cm", (B, G, dk), 2, G * dk, t, dev)
-    y = x.new_empty((B, H, dv)) if y is None else y
-    py, ldy = _rows(y, "y", (B, H, dv), 2, H * dv, t, dev)
-    hs = (H,)
-    cfg = lq_ssm_config(code, B, H, G, dk, dv, 1 if softplus else 0)
-    rc = lib().lq_ssm_step(C.addressof(cfg), _flat(S, "S", (B, H, dk, dv), dev), px, ldx, pd, ldd,
-                           _flat(A, "A", hs, dev), pb, ldb, pc, ldc, _flat(D, "D", hs, dev),
-                           _flat(dt_bias, "dt_bias", hs, dev), py, ldy, _raw_stream(dev))
-    _chk(rc, "lq_ssm_step")
-    return y
+    (allocated when None)."""
+    return _call("ssm_step", (S, x, dt, A, Bm, Cm, D, dt_bias, softplus, y), stream)
 
 
-@_layer_call
-def lq_norm_in(x, w, res=None, scale=1.0, eps=1e-5, h=None, y=None):
+def lq_norm_in(x, w, res=None, scale=1.0, eps=1e-5, h=None, y=None, stream=None):
     """Norm before a block, with the residual: h = res + scale x, y = rms(h) w
     over the last dimension of x [..., D]; scale is a number or a float32 tensor
-    [D].  Returns (y, h), allocated when None; h and y may be x or res.  Takes
-    stream=."""
-    t, dev, code = x.dtype, x.get_device(), _dtype_of(x)
-    shape = x.shape
-    D = shape[-1]
-    px, ldx = _rows(x, "x", shape, 1, D, t, dev)
-    pr, ldr = _rows(res, "res", shape, 1, D, t, dev) if res is not None else (None, 0)
-    h = x.new_empty(shape) if h is None else h
-    y = x.new_empty(shape) if y is None else y
-    ph, ldh = _rows(h, "h", shape, 1, D, t, dev)
-    py, ldy = _rows(y, "y", shape, 1, D, t, dev)
-    s, ps = _scale(scale, (D,), dev)
-    cfg = lq_norm_config(code, code, x.numel() // max(D, 1), 1, D, 0, 0, 0, eps, s)
-    rc = lib().lq_norm_in(C.addressof(cfg), px, ldx, _flat(w, "w", (D,), dev), pr, ldr, ps, ph, ldh, py, ldy,
-                          _raw_stream(dev))
-    _chk(rc, "lq_norm_in")
-    return y, h
+    [D].  Returns (y, h), allocated when None; h and y may be x or res."""
+    return _call("norm_in", (x, w, res, scale, eps, h, y), stream)
 
 
-@_layer_call
-def lq_norm_out(x, w, z=None, act="silu", gate_first=False, res=None, scale=1.0, eps=1e-5, y=None):
+def lq_norm_out(x, w, z=None, act="silu", gate_first=False, res=None, scale=1.0, eps=1e-5, y=None, stream=None):
     """Norm after a block, with its gate and the residual, over the last
     dimension of x [..., G, D] (x may be float32 beside 16-bit z, res and y):
     y = res + scale (rms(x) w act(z)), gate_first: res + scale (rms(x act(z)) w).
     w is [D] or [G, D]; scale a number or a float32 tensor [G, D].  The type of
-    y is that of a given y, z or res, else x's.  Returns y.  Takes stream=."""
-    t = y.dtype if y is not None else z.dtype if z is not None else res.dtype if res is not None else x.dtype
-    dev, shape = x.get_device(), x.shape
-    if len(shape) < 2:
-        raise ValueError(f"x is [..., G, D], got {tuple(shape)}")
-    G, D = shape[-2:]
-    xcode, n = _dtype_of(x), G * D
-    px, ldx = _rows(x, "x", shape, 2, n, x.dtype, dev)
-    pz, ldz = _rows(z, "z", shape, 2, n, t, dev) if z is not None else (None, 0)
-    pr, ldr = _rows(res, "res", shape, 2, n, t, dev) if res is not None else (None, 0)
-    y = x.new_empty(shape, dtype=t) if y is None else y
-    py, ldy = _rows(y, "y", shape, 2, n, t, dev)
-    wg = w.dim() == 2
-    s, ps = _scale(scale, (G, D), dev)
-    cfg = lq_norm_config(_dtype_of(y), xcode, x.numel() // max(n, 1), G, D, 1 if wg else 0, _act_of(act),
-                         1 if gate_first else 0, eps, s)
-    rc = lib().lq_norm_out(C.addressof(cfg), px, ldx, _flat(w, "w", (G, D) if wg else (D,), dev), pz, ldz, pr, ldr, ps,
-                           py, ldy, _raw_stream(dev))
-    _chk(rc, "lq_norm_out")
-    return y
+    y is that of a given y, z or res, else x's.  Returns y."""
+    return _call("norm_out", (x, w, z, act, gate_first, res, scale, eps, y), stream)
