@@ -68,16 +68,24 @@ struct Tiles {
     float B[Q][DK + 4];    // rows 4 banks apart: its columns' fragments without
     float X[Q][DV + 4];    // and the outputs, at the end
     float M[Q][Q + 8];
-    long long g[Q];        // log2 decay from the chunk's start (fixed point)
-    float d[Q], eg[Q], w[Q];   // steps, 2^g, weights in the next state
-    int first[DV];         // per value column, the first token whose x is not finite
-    float keep;            // 2^(g_Q)
+    // of even and odd chunks:
+    long long g[2][Q];     // log2 decay from the chunk's start (fixed point)
+    float d[2][Q], eg[2][Q], w[2][Q];   // steps, 2^g, weights in the next state
+    int first[2][DV];      // per value column, the first token whose x is not finite
+    float keep[2];         // 2^(g_Q)
 };
 
-// Q rows of W elements as floats (zeros from the sequence's end on).
+// Q rows of W elements as floats (zeros from the sequence's end on).  With first,
+// an element that is not finite is replaced by 0 (times 0 it would reach earlier
+// tokens) and its column marked from that token on.
 template <typename T, int W, int NT, int LD>
 __device__ __forceinline__ void load_rows(float (&dst)[Q][LD], const T *src, int64_t ld, const Piece &p, int t0,
-                                          bool vec) {
+                                          bool vec, int *first = nullptr) {
+    auto finite = [&](float v, int t, int c) {
+        if (fabsf(v) <= 3.402823466e38f) return v;
+        atomicMin(first + c, t);
+        return 0.0f;
+    };
     if (vec) {
 #pragma unroll
         for (int i = 0; i < Q * W / 8 / NT; ++i) {
@@ -87,6 +95,9 @@ __device__ __forceinline__ void load_rows(float (&dst)[Q][LD], const T *src, int
             else v.zero();
             float f[8];
             v.get(f);
+            if (first)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) f[k] = finite(f[k], t, 8 * j + k);
             float4 *o = reinterpret_cast<float4 *>(&dst[t][8 * j]);
             o[0] = make_float4(f[0], f[1], f[2], f[3]);
             o[1] = make_float4(f[4], f[5], f[6], f[7]);
@@ -94,7 +105,9 @@ __device__ __forceinline__ void load_rows(float (&dst)[Q][LD], const T *src, int
     } else {
         for (int e = threadIdx.x; e < Q * W; e += NT) {
             const int t = e / W, j = e % W;
-            dst[t][j] = t0 + t < p.len ? to_f<T>(src[(p.row0 + (int64_t)(t0 + t) * p.step) * ld + j]) : 0.0f;
+            float v = t0 + t < p.len ? to_f<T>(src[(p.row0 + (int64_t)(t0 + t) * p.step) * ld + j]) : 0.0f;
+            if (first) v = finite(v, t, j);
+            dst[t][j] = v;
         }
     }
 }
@@ -131,42 +144,43 @@ __global__ void __launch_bounds__(2 * DV, DV == 128 ? 2 : 4) ssm_tc_kernel(SsmAr
 #pragma unroll
         for (int e = 0; e < 4; ++e) S[i][e] = S0 ? S0[(8 * i + 2 * tq + (e & 1)) * DV + (e >> 1) * 8] : 0.0f;
 
-    long long gsum = 0;
+    // The last warp, whose share of the products before it is the least, forms the
+    // decays of the chunk at t, a chunk ahead.
+    const bool decays = warp == NW - 1;
     const int t_end = min(p.len, (p.j + 1) * seg);
-    for (int t0 = p.j * seg; t0 < t_end; t0 += Q) {
+    long long gsum = 0;
+    auto step_at = [&](int t) {
+        return t + lane < p.len ? to_f<T>(dp[(p.row0 + (int64_t)(t + lane) * p.step) * a.lddt]) : 0.0f;
+    };
+    auto form_decays = [&](float d, int t, int odd) {
+        long long gt = 0;
+        if (t + lane < p.len) {
+            d += bias;
+            if (a.softplus) d = softplus_f(d);
+            gt = decay_of(d, A2);
+        }
+        gt = warp_scan(gt);
+        const long long total = __shfl_sync(0xffffffffu, gt, 31);
+        s.g[odd][lane] = gt;
+        s.d[odd][lane] = d;
+        s.eg[odd][lane] = exp2f(decay_f(gt));
+        s.w[odd][lane] = d * exp2f(decay_f(total - gt));
+        if (lane == 0) s.keep[odd] = exp2f(decay_f(total));
+        gsum += total;
+    };
+    if (tid < DV) s.first[0][tid] = Q;
+    if (decays && p.j * seg < t_end) form_decays(step_at(p.j * seg), p.j * seg, 0);
+
+    int odd = 0;
+    for (int t0 = p.j * seg; t0 < t_end; t0 += Q, odd ^= 1) {
         __syncthreads();   // the chunk before is done with the tiles
+        const bool next = decays && t0 + Q < t_end;
+        const float dn = next ? step_at(t0 + Q) : 0.0f;
         load_rows<T, DK, NT>(s.B, bp, a.ldb, p, t0, vec);
-        load_rows<T, DV, NT>(s.X, xp, a.ldx, p, t0, vec);
+        load_rows<T, DV, NT>(s.X, xp, a.ldx, p, t0, vec, s.first[odd]);
         if (FULL) load_rows<T, DK, NT>(s.C, cp, a.ldc, p, t0, vec);
-        if (tid < DV) s.first[tid] = Q;
-        if (warp == 0) {
-            float d = 0.0f;
-            long long gt = 0;
-            if (t0 + lane < p.len) {
-                d = to_f<T>(dp[(p.row0 + (int64_t)(t0 + lane) * p.step) * a.lddt]) + bias;
-                if (a.softplus) d = softplus_f(d);
-                gt = decay_of(d, A2);
-            }
-            gt = warp_scan(gt);
-            const long long total = __shfl_sync(0xffffffffu, gt, 31);
-            s.g[lane] = gt;
-            s.d[lane] = d;
-            s.eg[lane] = exp2f(decay_f(gt));
-            s.w[lane] = d * exp2f(decay_f(total - gt));
-            if (lane == 0) s.keep = exp2f(decay_f(total));
-            gsum += total;
-        }
+        if (tid < DV) s.first[odd ^ 1][tid] = Q;
         __syncthreads();
-        // A non-finite x leaves X (times 0 it would reach earlier tokens): its
-        // column is marked from that token on.
-        for (int e = tid; e < Q * DV; e += NT) {
-            const int t = e / DV, c = e % DV;
-            const float v = s.X[t][c];
-            if (fabsf(v) > 3.402823466e38f || v != v) {
-                s.X[t][c] = 0.0f;
-                atomicMin(&s.first[c], t);
-            }
-        }
         if (FULL) {
             // lower 16 x 8 tiles of G, one at a time per warp
             for (int tile = warp; tile < 6; tile += NW) {
@@ -192,16 +206,17 @@ __global__ void __launch_bounds__(2 * DV, DV == 128 ? 2 : 4) ssm_tc_kernel(SsmAr
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int t = rb + gq + (e >> 1) * 8, u = cb + 2 * tq + (e & 1);
-                    s.M[t][u] = u <= t ? exp2f(decay_f(s.g[t] - s.g[u])) * s.d[u] * (acc[0][e] + acc[1][e] + low[e]) : 0.0f;
+                    s.M[t][u] = u <= t ? exp2f(decay_f(s.g[odd][t] - s.g[odd][u])) * s.d[odd][u] * (acc[0][e] + acc[1][e] + low[e]) : 0.0f;
                 }
             }
         }
+        if (next) form_decays(dn, t0 + Q, odd ^ 1);
         float Y[Q / 8][4] = {};   // Y^T tile j: value columns pc + gq (+8), tokens 8 j + 2 tq (+1)
         if (FULL) {
             constexpr int JS = PB == 1 ? Q / 8 : 2;   // token blocks at a time
 #pragma unroll
             for (int jb = 0; jb < Q / 8; jb += JS) {
-                float odd[JS][4] = {}, low[JS][4] = {};
+                float alt[JS][4] = {}, low[JS][4] = {};
 #pragma unroll
                 for (int i = 0; i < DK / 8; ++i) {
                     uint32_t ab[4], as[4];
@@ -211,23 +226,23 @@ __global__ void __launch_bounds__(2 * DV, DV == 128 ? 2 : 4) ssm_tc_kernel(SsmAr
                     for (int j = 0; j < JS; ++j) {
                         const float2 c = *reinterpret_cast<const float2 *>(&s.C[8 * (jb + j) + gq][8 * i + 2 * tq]);
                         if constexpr (PB == 1) mma_exact(Y[jb + j], ab, as, c.x, c.y);
-                        else mma_split(i & 1 ? odd[j] : Y[jb + j], low[j], ab, as, c.x, c.y);
+                        else mma_split(i & 1 ? alt[j] : Y[jb + j], low[j], ab, as, c.x, c.y);
                     }
                 }
                 if constexpr (PB == 2)
 #pragma unroll
                     for (int j = 0; j < JS; ++j)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) Y[jb + j][e] += odd[j][e] + low[j][e];
+                        for (int e = 0; e < 4; ++e) Y[jb + j][e] += alt[j][e] + low[j][e];
             }
 #pragma unroll
             for (int j = 0; j < Q / 8; ++j) {
-                const float e0 = s.eg[8 * j + 2 * tq], e1 = s.eg[8 * j + 2 * tq + 1];
+                const float e0 = s.eg[odd][8 * j + 2 * tq], e1 = s.eg[odd][8 * j + 2 * tq + 1];
                 Y[j][0] *= e0; Y[j][1] *= e1; Y[j][2] *= e0; Y[j][3] *= e1;
             }
         }
-        __syncthreads();   // M, and X without its non-finite values
-        const float keep = s.keep;
+        __syncthreads();   // M
+        const float keep = s.keep[odd];
         auto x_at = [&](int u, float (&x)[4]) {
             x[0] = s.X[u][pc + gq];
             x[1] = s.X[u][pc + gq + 8];
@@ -257,7 +272,7 @@ __global__ void __launch_bounds__(2 * DV, DV == 128 ? 2 : 4) ssm_tc_kernel(SsmAr
                         mma_tf32(Y[j], ar, mb[0], mb[1]);
                     }
                 }
-                const float w0 = s.w[u], w1 = s.w[u + 1];
+                const float w0 = s.w[odd][u], w1 = s.w[odd][u + 1];
                 const float xw[4] = {x[0] * w0, x[1] * w0, x[2] * w1, x[3] * w1};
                 uint32_t ab[4], as[4];
                 split4(xw, ab, as);
@@ -290,7 +305,7 @@ __global__ void __launch_bounds__(2 * DV, DV == 128 ? 2 : 4) ssm_tc_kernel(SsmAr
                     const int u = 8 * (kb + k) + 2 * tq;
                     float x[4];
                     x_at(u, x);
-                    const float w0 = s.w[u], w1 = s.w[u + 1];
+                    const float w0 = s.w[odd][u], w1 = s.w[odd][u + 1];
                     const float xw[4] = {x[0] * w0, x[1] * w0, x[2] * w1, x[3] * w1};
                     split4(xw, ab[k], as[k]);
                 }
@@ -308,7 +323,7 @@ __global__ void __launch_bounds__(2 * DV, DV == 128 ? 2 : 4) ssm_tc_kernel(SsmAr
             }
         }
         // from a non-finite x on, its column has no finite state
-        const int f0 = s.first[pc + gq], f1 = s.first[pc + gq + 8];
+        const int f0 = s.first[odd][pc + gq], f1 = s.first[odd][pc + gq + 8];
         const float nan = __int_as_float(0x7fffffff);
         if (f0 < Q || f1 < Q)
 #pragma unroll
@@ -354,7 +369,7 @@ __global__ void __launch_bounds__(2 * DV, DV == 128 ? 2 : 4) ssm_tc_kernel(SsmAr
 #pragma unroll
             for (int e = 0; e < 4; ++e) so[(8 * i + 2 * tq + (e & 1)) * DV + (e >> 1) * 8] = S[i][e];
     }
-    if (!FULL && tid == 0) ssm_decays(a, seg)[p.id * a.H + h] = exp2f(decay_f(gsum));
+    if (!FULL && tid == NT - 32) ssm_decays(a, seg)[p.id * a.H + h] = exp2f(decay_f(gsum));
 }
 
 template <typename T, int DK, int DV>
