@@ -11,8 +11,10 @@
 //   S^T <- 2^(g_Q) S^T + X'^T B,  X'[s] = 2^(g_Q - g_s) d_s X[s]
 // f16 operands are exact in TF32; S, M and X' (and f32 operands) enter as two
 // TF32 parts, big x big + big x small + small x big: about 2^-22 of a term.
-// Bound: latency of the MMA chains and the barriers between them, two to four
-// CTAs per SM.
+// Bound: with few CTAs latency (a chunk of a 64 x 64 head 10000 cycles, f32: rows
+// 2000, G 2600, C S 1900, M X and the state 2700), with many the rate of mma.sync:
+// two CTAs per SM for 128 value columns, four for 64.  3001 f16 tokens of 6 heads
+// of 64 x 128: 37 us; 16384 f32 tokens of 16 heads of 128 x 128: 832 us.
 #include "lq_ssm.h"
 
 namespace lq {
@@ -213,28 +215,27 @@ __global__ void __launch_bounds__(2 * DV, DV == 128 ? 2 : 4) ssm_tc_kernel(SsmAr
         if (next) form_decays(dn, t0 + Q, odd ^ 1);
         float Y[Q / 8][4] = {};   // Y^T tile j: value columns pc + gq (+8), tokens 8 j + 2 tq (+1)
         if (FULL) {
-            constexpr int JS = PB == 1 ? Q / 8 : 2;   // token blocks at a time
+            // (All token blocks in one pass over S: taken two at a time, S's parts are
+            // kept for the second pass and spill, 944 us against 832 for 16384 tokens of
+            // 16 f32 heads of 128 x 128.)
+            float alt[Q / 8][4] = {}, low[Q / 8][4] = {};
 #pragma unroll
-            for (int jb = 0; jb < Q / 8; jb += JS) {
-                float alt[JS][4] = {}, low[JS][4] = {};
+            for (int i = 0; i < DK / 8; ++i) {
+                uint32_t ab[4], as[4];
+                const float sv[4] = {S[i][0], S[i][2], S[i][1], S[i][3]};
+                split4(sv, ab, as);
 #pragma unroll
-                for (int i = 0; i < DK / 8; ++i) {
-                    uint32_t ab[4], as[4];
-                    const float sv[4] = {S[i][0], S[i][2], S[i][1], S[i][3]};
-                    split4(sv, ab, as);
-#pragma unroll
-                    for (int j = 0; j < JS; ++j) {
-                        const float2 c = *reinterpret_cast<const float2 *>(&s.C[8 * (jb + j) + gq][8 * i + 2 * tq]);
-                        if constexpr (PB == 1) mma_exact(Y[jb + j], ab, as, c.x, c.y);
-                        else mma_split(i & 1 ? alt[j] : Y[jb + j], low[j], ab, as, c.x, c.y);
-                    }
+                for (int j = 0; j < Q / 8; ++j) {
+                    const float2 c = *reinterpret_cast<const float2 *>(&s.C[8 * j + gq][8 * i + 2 * tq]);
+                    if constexpr (PB == 1) mma_exact(Y[j], ab, as, c.x, c.y);
+                    else mma_split(i & 1 ? alt[j] : Y[j], low[j], ab, as, c.x, c.y);
                 }
-                if constexpr (PB == 2)
-#pragma unroll
-                    for (int j = 0; j < JS; ++j)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) Y[jb + j][e] += alt[j][e] + low[j][e];
             }
+            if constexpr (PB == 2)
+#pragma unroll
+                for (int j = 0; j < Q / 8; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) Y[j][e] += alt[j][e] + low[j][e];
 #pragma unroll
             for (int j = 0; j < Q / 8; ++j) {
                 const float e0 = s.eg[odd][8 * j + 2 * tq], e1 = s.eg[odd][8 * j + 2 * tq + 1];
