@@ -165,14 +165,17 @@ Rows rows_or_none(PyObject *o, const char *name, IntArrayRef shape, int n_tail, 
     return o == Py_None ? Rows{} : rows(o, name, shape, n_tail, width, type, dev);
 }
 
-// An optional contiguous tensor.
+// A contiguous tensor (flat: or None).
 template <typename T = float>
-T *flat(PyObject *o, const char *name, IntArrayRef shape, int dev, ScalarType type = at::kFloat) {
-    if (o == Py_None) return nullptr;
+T *given(PyObject *o, const char *name, IntArrayRef shape, int dev, ScalarType type = at::kFloat) {
     const Tensor &t = tensor(o, name, dev);
     check(t, name, shape, type);
     if (!t.is_contiguous()) refuse(PyExc_ValueError, "%s must be contiguous", name);
     return static_cast<T *>(t.data_ptr());
+}
+template <typename T = float>
+T *flat(PyObject *o, const char *name, IntArrayRef shape, int dev, ScalarType type = at::kFloat) {
+    return o == Py_None ? nullptr : given<T>(o, name, shape, dev, type);
 }
 
 // An output: the given tensor or a new one of the first argument's device.
@@ -293,7 +296,7 @@ PyObject *ssm_prefill(PyObject *const *a) {
     const Shape st{pr.B, H, dk, dv};
     const Rows px = rows(x, "x", sx, 2, H * dv, t), pd = rows(a[1], "dt", sd, 1, H, t, dev.id);
     const Rows pb = rows(a[3], "Bm", sb, 2, G * dk, t, dev.id), pc = rows(a[4], "Cm", sb, 2, G * dk, t, dev.id);
-    const float *A = flat(a[2], "A", {H}, dev.id), *D = flat(a[5], "D", {H}, dev.id);
+    const float *A = given(a[2], "A", {H}, dev.id), *D = flat(a[5], "D", {H}, dev.id);
     const float *bias = flat(a[6], "dt_bias", {H}, dev.id), *S0 = flat(a[8], "S0", st, dev.id);
     const lq_ssm_config cfg{code, pr.B, i32(H), i32(G), i32(dk), i32(dv), truth(a[7]) ? 1 : 0};
     Out y(a[10], x, sx, t), So(a[9], x, st, at::kFloat);
@@ -329,7 +332,7 @@ PyObject *ssm_step(PyObject *const *a) {
     const Rows px = rows(x, "x", {B, H, dv}, 2, H * dv, t), pd = rows(a[2], "dt", {B, H}, 1, H, t, dev.id);
     const Rows pb = rows(a[4], "Bm", {B, G, dk}, 2, G * dk, t, dev.id);
     const Rows pc = rows(a[5], "Cm", {B, G, dk}, 2, G * dk, t, dev.id);
-    const float *A = flat(a[3], "A", {H}, dev.id), *D = flat(a[6], "D", {H}, dev.id);
+    const float *A = given(a[3], "A", {H}, dev.id), *D = flat(a[6], "D", {H}, dev.id);
     const float *bias = flat(a[7], "dt_bias", {H}, dev.id);
     float *S = flat(a[0], "S", {B, H, dk, dv}, dev.id);
     const lq_ssm_config cfg{code, i32(B), i32(H), i32(G), i32(dk), i32(dv), truth(a[8]) ? 1 : 0};
@@ -361,7 +364,7 @@ PyObject *norm_in(PyObject *const *a) {
     const int64_t D = x.size(-1);
     const Rows px = rows(x, "x", sx, 1, D, t), pr = rows_or_none(a[2], "res", sx, 1, D, t, dev.id);
     float factor;
-    const float *w = flat(a[1], "w", {D}, dev.id), *ps = scale_of(a[3], {D}, dev.id, factor);
+    const float *w = given(a[1], "w", {D}, dev.id), *ps = scale_of(a[3], {D}, dev.id, factor);
     const lq_norm_config cfg{code, code, i32(x.numel() / std::max<int64_t>(D, 1)), 1, i32(D), 0, 0, 0,
                              (float)number(a[4]), factor};
     Out h(a[5], x, sx, t), y(a[6], x, sx, t);

@@ -26,6 +26,9 @@ struct Span {
 Span rows_of(const void *p, int64_t n, int64_t width, int64_t ld, int size) {
     return {reinterpret_cast<uintptr_t>(p), n, width * size, ld * size};
 }
+Span offsets(const Rows &r) {
+    return {reinterpret_cast<uintptr_t>(r.cu), 1, ((int64_t)r.B + 1) * 4, ((int64_t)r.B + 1) * 4};
+}
 Span flat(const void *p, int64_t bytes) { return {reinterpret_cast<uintptr_t>(p), bytes > 0 ? 1 : 0, bytes, bytes}; }
 
 // Whether two arrays may share bytes.  Apart in memory, or different columns of
@@ -97,7 +100,7 @@ int check_ssm_arrays(const lq_ssm_config *c, const lq::SsmArgs &a) {
     const Span in[] = {rows_of(a.x, n, wx, a.ldx, e),   rows_of(a.dt, n, c->H, a.lddt, e),
                        rows_of(a.Bm, n, wb, a.ldb, e),  rows_of(a.Cm, n, wb, a.ldc, e),
                        flat(a.A, (int64_t)c->H * 4),    flat(a.D, (int64_t)c->H * 4),
-                       flat(a.dt_bias, (int64_t)c->H * 4)};
+                       flat(a.dt_bias, (int64_t)c->H * 4), offsets(a.r)};
     const Span y = rows_of(a.y, n, wx, a.ldy, e), S = flat(a.S_out, sb), S0 = flat(a.S0, sb);
     for (const Span &i : in)
         if (overlap(i, y) || overlap(i, S)) return LQ_ERR_INVALID_ARG;
@@ -179,11 +182,11 @@ int lq_conv_prefill(const lq_conv_config *cfg, int32_t rows, const int32_t *d_cu
     const Span x = rows_of(d_x, rows, cfg->C, ldx, e), y = rows_of(d_y, rows, cfg->C, ldy, e);
     const Span s0 = flat(d_state0, sb), so = flat(d_state_out, sb);
     const Span w = flat(d_w, (int64_t)cfg->C * cfg->K * 4), bias = flat(d_bias, (int64_t)cfg->C * 4);
-    for (const Span &o : {y, so})
-        if (overlap(o, x) || overlap(o, w) || overlap(o, bias)) return LQ_ERR_INVALID_ARG;
-    if (overlap(y, s0) || overlap(y, so) || (overlap(s0, so) && d_state0 != d_state_out)) return LQ_ERR_INVALID_ARG;
     lq::ConvArgs a{};
     a.r.cu = d_cu; a.r.B = cfg->B; a.r.rows = rows;
+    for (const Span &o : {y, so})
+        if (overlap(o, x) || overlap(o, w) || overlap(o, bias) || overlap(o, offsets(a.r))) return LQ_ERR_INVALID_ARG;
+    if (overlap(y, s0) || overlap(y, so) || (overlap(s0, so) && d_state0 != d_state_out)) return LQ_ERR_INVALID_ARG;
     a.C = cfg->C; a.K = cfg->K; a.act = cfg->act;
     a.x = d_x; a.ldx = ldx; a.w = d_w; a.bias = d_bias;
     a.state0 = d_state0; a.state_out = d_state_out;
@@ -244,7 +247,9 @@ int lq_ssm_prefill(const lq_ssm_config *cfg, int32_t rows, const int32_t *d_cu, 
         const Span ws = flat(d_ws, (int64_t)need);
         const Span other[] = {rows_of(d_x, rows, wx, ldx, e),  rows_of(d_dt, rows, cfg->H, lddt, e),
                               rows_of(d_Bm, rows, wb, ldb, e), rows_of(d_Cm, rows, wb, ldc, e),
-                              rows_of(d_y, rows, wx, ldy, e),  flat(d_S0, sb), flat(d_S_out, sb)};
+                              rows_of(d_y, rows, wx, ldy, e),  flat(d_S0, sb), flat(d_S_out, sb),
+                              flat(d_A, (int64_t)cfg->H * 4),  flat(d_D, (int64_t)cfg->H * 4),
+                              flat(d_dt_bias, (int64_t)cfg->H * 4), offsets(a.r)};
         for (const Span &o : other)
             if (overlap(ws, o)) return LQ_ERR_INVALID_ARG;
         a.ws = static_cast<float *>(d_ws);

@@ -444,7 +444,7 @@ def lq_state_destroy(st: LqState):
 # state-space scan, norms.  Activations float32, bfloat16 or float16; prompts
 # are packed ([rows, ...] with cu, the B+1 int32 row offsets on the device) or
 # time-major ([T, B, ...]); rows may be columns of a wider tensor.  Calls run on
-# torch's current stream of their first argument's device, or on stream=.
+# torch's current stream of their first argument's device, or on stream=.  They record no gradients.
 # ---------------------------------------------------------------------------
 LQ_F32, LQ_BF16, LQ_F16 = 0, 1, 2
 LQ_ACT_NONE, LQ_ACT_SILU, LQ_ACT_SIGMOID = 0, 1, 2

@@ -470,6 +470,53 @@ def test_norms_in_place_and_zero_rows():
 
 # -- streams, graphs, chains ----------------------------------------------------------
 
+def test_binding_refuses_what_it_cannot_pass_on():
+    """Tensors of another type, shape, spacing or device, unknown names and sizes
+    beyond 32 bits are refused before anything is allocated or launched."""
+    _gpu()
+    z = lambda *s, t=BF16: torch.zeros(s, dtype=t, device="cuda")   # noqa: E731
+    x, w, h = z(6, 2, 64), z(64, 4, t=F32), z(6, 2, 2, 64)
+    dt, A, S, B1 = z(6, 2, 2), z(2, t=F32), z(2, 2, 64, 64, t=F32), z(6, 2, 1, 64)
+    cu = torch.tensor([0, 6], dtype=torch.int32, device="cuda")
+    wrong_type = [
+        lambda: lq.lq_conv_prefill(x.double(), w), lambda: lq.lq_conv_prefill(x, w.half()),
+        lambda: lq.lq_conv_prefill(x, w.cpu()), lambda: lq.lq_conv_prefill(x, w, bias=3.0),
+        lambda: lq.lq_conv_prefill(x[:, 0], w, cu=cu.long()), lambda: lq.lq_conv_prefill(x[:, 0], w, cu=[0, 6]),
+        lambda: lq.lq_conv_step(z(2, 3, 64, t=F32), x[0], w), lambda: lq.lq_ssm_prefill(h, dt.float(), A, B1, B1),
+        lambda: lq.lq_ssm_prefill(h, dt, A, B1, B1, S0=S.bfloat16()), lambda: lq.lq_ssm_step(S, h[0], dt[0], A, B1[0], 1),
+        lambda: lq.lq_norm_in(x, w[:, 0].contiguous(), res=x.float()), lambda: lq.lq_norm_in(x, None),
+        lambda: lq.lq_norm_in(x, w[:, 0].contiguous(), scale="1"), lambda: lq.lq_norm_out(x, w[:, 0].contiguous(), z=3),
+        lambda: lq.lq_norm_out(x, w[:, 0].contiguous(), z=x.half(), res=x),
+    ]
+    wrong_value = [
+        lambda: lq.lq_conv_prefill(x, w[:32]), lambda: lq.lq_conv_prefill(x, w, act="relu"),
+        lambda: lq.lq_conv_prefill(x, w[0]), lambda: lq.lq_conv_prefill(x[:, 0], w), lambda: lq.lq_conv_prefill(x, w, cu=cu),
+        lambda: lq.lq_conv_prefill(x[:, 0], w, cu=cu[:1]), lambda: lq.lq_conv_prefill(x, w[:, ::2]),
+        lambda: lq.lq_conv_prefill(z(6, 2, 128)[..., ::2], w), lambda: lq.lq_conv_prefill(z(12, 4, 64)[::2, ::2][:, :2], w, y=x[:5]),
+        lambda: lq.lq_conv_prefill(z(6, 3, 64)[:, :2], w), lambda: lq.lq_conv_step(z(2, 3, 32), x[0], w),
+        lambda: lq.lq_ssm_prefill(h, dt[:5], A, B1, B1), lambda: lq.lq_ssm_prefill(h, dt, A, B1, B1[..., :32]),
+        lambda: lq.lq_ssm_prefill(h, dt, A[:1], B1, B1), lambda: lq.lq_ssm_step(S[:1], h[0], dt[0], A, B1[0], B1[0]),
+        lambda: lq.lq_ssm_step(S.transpose(2, 3), h[0], dt[0], A, B1[0], B1[0]),
+        lambda: lq.lq_norm_in(x, w[:32, 0].contiguous()), lambda: lq.lq_norm_in(x, w[:, 0]),
+        lambda: lq.lq_norm_out(x, w[:, 0].contiguous(), scale=w[:, 0].contiguous()),
+        lambda: lq.lq_norm_out(x[0, 0], w[:, 0].contiguous()),
+    ]
+    for n, call in enumerate(wrong_type):
+        with pytest.raises(TypeError):
+            call()
+            pytest.fail(f"type {n}")
+    for n, call in enumerate(wrong_value):
+        with pytest.raises(ValueError):
+            call()
+            pytest.fail(f"value {n}")
+    with pytest.raises(lq.LqError) as e:
+        lq.lq_ssm_prefill(z(6, 2, 2, 32), dt, A, B1, B1)
+    assert e.value.code == lq.LQ_ERR_UNSUPPORTED
+    with pytest.raises(lq.LqError) as e:
+        lq.lq_conv_prefill(x, w, y=x)
+    assert e.value.code == lq.LQ_ERR_INVALID_ARG
+
+
 def test_side_stream_and_graph_replay():
     """Calls on a stream of the caller's, and captured and replayed, give the
     eager call's bits."""

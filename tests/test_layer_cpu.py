@@ -34,6 +34,7 @@ def conv(cfg=None, **kw):
     ({}, {"x": None}, lq.LQ_ERR_INVALID_ARG), ({}, {"y": None}, lq.LQ_ERR_INVALID_ARG),
     ({}, {"w": None}, lq.LQ_ERR_INVALID_ARG), ({}, {"x": at(0, 1)}, lq.LQ_ERR_INVALID_ARG),
     ({}, {"ldx": 63}, lq.LQ_ERR_SHAPE), ({}, {"ldy": 0}, lq.LQ_ERR_SHAPE), ({}, {"ldx": 1 << 40}, lq.LQ_ERR_SHAPE),
+    ({}, {"cu": at(5)}, lq.LQ_ERR_INVALID_ARG), ({}, {"cu": at(4, 8)}, lq.LQ_ERR_INVALID_ARG),
     ({}, {"y": at(0)}, lq.LQ_ERR_INVALID_ARG),                         # y over x
     ({}, {"y": at(0, 64), "ldx": 96, "ldy": 96}, lq.LQ_ERR_INVALID_ARG),   # columns that meet
     ({}, {"so": at(3, 128)}, lq.LQ_ERR_INVALID_ARG),                   # windows partly over each other
@@ -90,7 +91,8 @@ def test_ssm_refuses(cfg, kw, code, step):
 
 @pytest.mark.parametrize("cfg,kw,code", [
     ({"B": 3}, {}, lq.LQ_ERR_SHAPE), ({}, {"rows": -1}, lq.LQ_ERR_INVALID_ARG),
-    ({}, {"S0": at(6, 64)}, lq.LQ_ERR_INVALID_ARG), ({}, {"y": at(5)}, lq.LQ_ERR_INVALID_ARG)])
+    ({}, {"S0": at(6, 64)}, lq.LQ_ERR_INVALID_ARG), ({}, {"y": at(5)}, lq.LQ_ERR_INVALID_ARG),
+    ({}, {"cu": at(6)}, lq.LQ_ERR_INVALID_ARG), ({}, {"cu": at(7, 4)}, lq.LQ_ERR_INVALID_ARG)])
 def test_ssm_prefill_refuses(cfg, kw, code):
     assert ssm(False, cfg, **kw) == code
 
@@ -106,6 +108,8 @@ def test_ssm_workspace_is_checked():
     assert ssm(False, one, rows=5000, ws=at(8, 16), n=need) == lq.LQ_ERR_WORKSPACE
     assert ssm(False, one, rows=5000, ws=at(8), n=need - 1) == lq.LQ_ERR_WORKSPACE
     assert ssm(False, one, rows=5000, ws=at(7), n=need) == lq.LQ_ERR_INVALID_ARG
+    assert ssm(False, one, rows=5000, ws=at(2), n=need) == lq.LQ_ERR_INVALID_ARG
+    assert ssm(False, one, rows=5000, cu=at(8), ws=at(8), n=need) == lq.LQ_ERR_INVALID_ARG
     assert lq.lq_ssm_workspace_bytes(torch.bfloat16, 1, 4, 2, 128, 64, 5000) == need
 
 
