@@ -287,7 +287,8 @@ struct Steps {
 // warp finds the next one and sends for its first tiles before the last one ends.
 template <int DK, int HPC>
 __global__ void __launch_bounds__(kNT, 1)
-    ssm_umma_kernel(SsmArgs a, const __grid_constant__ SsmMaps maps, int seg, int tma, int split) {
+    ssm_umma_kernel(SsmArgs a, const __grid_constant__ SsmMaps maps, int seg, int tma, int split,
+                    int direct) {
     constexpr int DV = 128 / HPC;
     // Tensor memory: G at 0, Y with C S's first part at 128, its second at 256.
     // One head: M over G, the state's products at 384.  Two: M of the first at
@@ -363,6 +364,25 @@ __global__ void __launch_bounds__(kNT, 1)
         if (lane == 0) fx.walk = w;
         __syncwarp();
     };
+    auto place = [&](Item &it) {
+        it.t_first = it.p.j * seg;
+        it.t_end = min(it.p.len, it.t_first + seg);
+        it.tm_t = a.r.cu ? (int)it.p.row0 : 0;
+        it.tm_b = a.r.cu ? 0 : it.p.b;
+    };
+    // No more items than CTAs: this one's is found without the walk (3000 cycles).
+    auto only_item = [&]() {
+        const int z = (int)(blockIdx.x / (unsigned)units);
+        Item it;
+        it.valid = find_piece(a.r, seg, z, it.p) && it.p.len > 0;
+        it.u = unit_of<HPC>((int)(blockIdx.x - (unsigned)z * units), a.H, a.G);
+        place(it);
+        if (lane == 0) {
+            fx.item[0] = it;
+            fx.walk = Walk{};
+        }
+        __syncwarp();
+    };
     auto next_item = [&](Item &out) {
         Walk w = fx.walk;
         Item it;
@@ -387,10 +407,7 @@ __global__ void __launch_bounds__(kNT, 1)
             it.p.step = a.r.cu ? 1 : a.r.B;
             it.p.id = (a.r.cu ? c0 / seg + w.b : (int64_t)w.b * n) + w.j;
             it.u = unit_of<HPC>(w.u++, a.H, a.G);
-            it.t_first = w.j * seg;
-            it.t_end = min(len, it.t_first + seg);
-            it.tm_t = a.r.cu ? c0 : 0;
-            it.tm_b = a.r.cu ? 0 : w.b;
+            place(it);
             w.pos += (it.t_end - it.t_first + Q - 1) / Q;
         }
         __syncwarp();
@@ -438,8 +455,12 @@ __global__ void __launch_bounds__(kNT, 1)
     };
 
     if (finder) {
-        start_walk();
-        next_item(fx.item[0]);
+        if (direct) {
+            only_item();
+        } else {
+            start_walk();
+            next_item(fx.item[0]);
+        }
         if (lane == 0) {
             for (int i = 0; i < 8; ++i) mbar_init(&fx.bar[i], 1);
             fx.bad = 0;
@@ -1110,7 +1131,8 @@ cudaError_t launch(const SsmArgs &a, const SsmMaps &maps, int seg, int tma, int 
         e = launch_ssm_join(a, seg, s);
         if (e != cudaSuccess) return e;
     }
-    ssm_umma_kernel<DK, HPC><<<grid(piece_count(a.r, seg) * units), kNT, bytes, s>>>(a, maps, seg, tma, split);
+    const int64_t items = piece_count(a.r, seg) * units;
+    ssm_umma_kernel<DK, HPC><<<grid(items), kNT, bytes, s>>>(a, maps, seg, tma, split, items <= kSms);
     return cudaGetLastError();
 }
 
