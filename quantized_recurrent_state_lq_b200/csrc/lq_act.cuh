@@ -271,7 +271,15 @@ __device__ __forceinline__ bool find_cut(const Rows &r, int seg, int k, Piece &p
         return b < r.B && find_piece(r, seg, b * (cuts + 1) + k % cuts, p);
     }
     const int b = last_sequence(r, seg, 0, k);
-    return k >= cu_at(r, b) / seg && find_piece(r, seg, k + b, p) && p.b == b && p.j < p.n - 1;
+    const int c0 = cu_at(r, b), c1 = max(cu_at(r, b + 1), c0);
+    p.b = b;
+    p.j = k - c0 / seg;
+    p.id = k + b;
+    p.len = c1 - c0;
+    p.n = max(1, (p.len + seg - 1) / seg);
+    p.row0 = c0;
+    p.step = 1;
+    return p.j >= 0 && p.j < p.n - 1;
 }
 
 __host__ __device__ inline int64_t piece_count(const Rows &r, int seg) {

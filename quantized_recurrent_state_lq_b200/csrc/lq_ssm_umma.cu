@@ -923,7 +923,6 @@ __global__ void __launch_bounds__(kNT + 32, 1)
     const int hh = HPC == 2 ? cq >> 1 : 0, j0 = cq * (CW / 8);
     const bool issuer = wid == kNT / 32, lead = ti == kNT;
     const int units = unit_count<HPC>(a.H, a.G), chunks = seg / Q;
-    const int64_t sall = (int64_t)a.H * DK * DV;
     auto b_tile = [&](int n) { return sm + (n & 1 ? kOffB : kOffC); };
     uint64_t *x_bar = &fx.bar[2], *mma_bar = &fx.bar[3];   // and bar[0], bar[1]: B of even and odd chunks
 
@@ -938,6 +937,10 @@ __global__ void __launch_bounds__(kNT + 32, 1)
             reinterpret_cast<uint4 *>(sm + kOffB + kBlk)[i] = reinterpret_cast<uint4 *>(sm + kOffC + kBlk)[i] =
                 make_uint4(0u, 0u, 0u, 0u);
     }
+    Piece p;   // the first item's, while tensor memory is allocated
+    int64_t at = blockIdx.x;
+    int z = (int)(at / units);
+    bool found = find_cut(a.r, seg, z, p);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -946,10 +949,8 @@ __global__ void __launch_bounds__(kNT + 32, 1)
     // (The issuing warp meets the others at the same barriers from code of its own.)
     auto sync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(kNT + 32) : "memory"); };
     int n = 0;   // chunks so far: the barriers' phases
-    for (int64_t at = blockIdx.x; at < items; at += gridDim.x) {
-        const int z = (int)(at / units);
-        Piece p;
-        if (!find_cut(a.r, seg, z, p)) continue;
+    for (; at < items; at += gridDim.x, z = (int)(at / units), found = at < items && find_cut(a.r, seg, z, p)) {
+        if (!found) continue;
         const Unit u = unit_of<HPC>((int)(at - (int64_t)z * units), a.H, a.G);
         const bool active = hh < u.heads;
         const int t_first = p.j * seg;
@@ -990,6 +991,15 @@ __global__ void __launch_bounds__(kNT + 32, 1)
             }
             if (!mbar_wait_bounded(mma_bar, (n - 1) & 1, nullptr)) fx.bad = 1;
             sync();   // every wait is over
+            sync();   // the state is where X' was
+            if (lead) {
+                const int64_t head = p.id * a.H + u.h;
+                for (int c = 0; c < u.heads * (DV / CW); ++c)
+                    tma_store_state(&maps.ws, sm + kOffU + c * kBlk, c * CW % DV, (int)((head + c * CW / DV) * DK));
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            }
+            __syncwarp();
             if (fx.bad) break;
             continue;
         }
@@ -1059,19 +1069,23 @@ __global__ void __launch_bounds__(kNT + 32, 1)
         update_state(S, tl + ((n - 1) & 1) * 128 + cq * CW, keep_before);
         tc_fence_before();
         sync();   // every wait is over
-        if (r < DK && active) {
-            float4 *so = reinterpret_cast<float4 *>(a.ws + p.id * sall + ((int64_t)(u.h + hh) * DK + r) * DV + cq * CW -
-                                                    hh * DV);
-            const float nan = __int_as_float(0x7fffffff);   // a wait that ran out leaves no state that looks like one
+        const bool bad = fx.bad;   // a wait that ran out leaves no state that looks like one
+        if (r < DK) {
 #pragma unroll
-            for (int i = 0; i < CW / 4; ++i)
-                so[i] = fx.bad ? make_float4(nan, nan, nan, nan)
-                               : make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+            for (int i = 0; i < CW / 4; ++i) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[k] = bad ? 0x7fffffffu : __float_as_uint(S[4 * i + k]);
+                *chunk(sm + kOffU + cq * kBlk, r, i) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
         }
+        fence_async_smem();
+        sync();
         if (active && r == 0 && (HPC == 2 ? (cq & 1) : cq) == 0)
             ssm_decays(a, seg)[p.id * a.H + u.h + hh] = exp2f(decay_f(gsum));
-        if (fx.bad) break;
+        if (bad) break;
     }
+    if (lead) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     tc_fence_before();
     __syncthreads();
     if (wid == 2) {
