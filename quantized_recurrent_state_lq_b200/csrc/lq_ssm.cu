@@ -11,6 +11,8 @@
 // times the CTAs, a quarter of the serial work each).  The state stays in
 // registers over the tokens of a short prompt.  256 sequences of 32 heads of
 // 128 x 128 (1.07 GB): 163 us, the copy rate.
+#include <algorithm>
+
 #include "lq_ssm.h"
 
 namespace lq {
@@ -164,23 +166,59 @@ __global__ void __launch_bounds__(kJoinThreads) ssm_join_kernel(SsmArgs a, int s
     }
 }
 
-// Tokens per piece: pieces are cut so that the batch gives about as many CTAs
-// as the GPU runs side by side -- for bf16 one per SM and 128 value columns, else
-// a head each, two per SM for 128 value columns and four for 64 (16384 tokens of 16
-// heads of 64 x 64: 273 us against 407 with two).  A batch with enough sequences
-// and heads is cut only where a sequence is longer than a CTA's share of all
-// tokens.  Pieces hold whole chunks, down to a single one.
-int piece_tokens(const Rows &r, int dtype, int H, int G, int dv) {
-    int64_t units = H, slots = dv == 64 ? 148 * 4 : 148 * 2, chunk = 32;
-    if (dtype == kBF16) {
+// What runs side by side: for bf16 one CTA per SM and 128 value columns, else a
+// head each, two per SM for 128 value columns and four for 64 (16384 tokens of 16
+// heads of 64 x 64: 273 us against 407 with two).
+struct Fit {
+    int64_t units, slots, chunk;
+    Fit(int dtype, int H, int G, int dv) : units(H), slots(dv == 64 ? 148 * 4 : 148 * 2), chunk(32) {
+        if (dtype != kBF16) return;
         slots = 148;
         chunk = 128;
         if (dv == 64) units = (int64_t)G * ((H / G + 1) / 2);
     }
-    const int64_t share = units <= slots ? (r.rows + slots / units - 1) / (slots / units)
-                                         : (r.rows * units + slots - 1) / slots;
-    const int64_t seg = (share + chunk - 1) / chunk * chunk;
-    return (int)(seg < chunk ? chunk : seg > (1 << 30) ? (1 << 30) : seg);
+};
+
+// Tokens per piece of sequences of unknown lengths: pieces are cut so that the
+// batch gives about as many CTAs as the GPU runs side by side.  A batch with enough
+// sequences and heads is cut only where a sequence is longer than a CTA's share of
+// all tokens.  Pieces hold whole chunks, down to a single one.
+int ragged_piece(const Fit &f, int64_t rows) {
+    const int64_t share = f.units <= f.slots ? (rows + f.slots / f.units - 1) / (f.slots / f.units)
+                                             : (rows * f.units + f.slots - 1) / f.slots;
+    const int64_t seg = (share + f.chunk - 1) / f.chunk * f.chunk;
+    return (int)(seg < f.chunk ? f.chunk : seg > (1 << 30) ? (1 << 30) : seg);
+}
+
+// The same of B equal sequences of T tokens, by the chunk times that it takes.  A cut
+// costs two launches and the pieces' own states at a third (by mma.sync 0.45) of a
+// chunk's time.  bf16: not cut, or in as many pieces as give each CTA one, or one more
+// or half as many; more pieces than CTAs leave some CTAs with part of a piece more
+// than their share.  (16000 tokens of 10 sequences, 8 heads of 128 x 128: 90 us uncut,
+// 128 cut.)  f32, f16: not cut, or as above -- several CTAs share an SM, whose rate is
+// what counts.  (3000 tokens of 20 sequences, 24 f32 heads of 64 x 64: 65 and 107 us.)
+int even_piece(const Fit &f, int dtype, int64_t B, int64_t T) {
+    const int64_t n = (T + f.chunk - 1) / f.chunk, all = B * f.units;
+    if (dtype != kBF16) {
+        const int seg = ragged_piece(f, B * T);
+        const float share = (float)all * (float)n / (float)f.slots, len = (float)(seg / f.chunk);
+        return (float)n <= 1.8f + 1.45f * std::max(share, len) ? (int)(n * f.chunk) : seg;
+    }
+    const int64_t fill = f.slots / all;
+    int64_t best = n;
+    float least = 3.0e38f;
+    for (int64_t m : {(int64_t)1, fill / 2, fill, fill + 1}) {
+        m = std::max((int64_t)1, std::min(m, n));
+        const int64_t len = (n + m - 1) / m, cut = (n + len - 1) / len;   // chunks, pieces
+        const int64_t waves = (all * (cut - 1) + f.slots - 1) / f.slots;
+        float time = all * cut <= f.slots ? (float)len : (float)all * (float)n / (float)f.slots + 0.75f * (float)len;
+        if (cut > 1) time += 1.8f + 0.33f * (float)(waves * len);
+        if (time < least) {
+            least = time;
+            best = len;
+        }
+    }
+    return (int)(best * f.chunk);
 }
 
 // Sequences of at most this length are not cut: the two launches more cost what
@@ -210,17 +248,30 @@ bool token_by_token(const Rows &r) {
 }
 
 size_t ssm_ws_bytes(int dtype, int B, int rows, int H, int G, int dk, int dv) {
-    Rows r{nullptr, B, rows};
-    const int seg = piece_tokens(r, dtype, H, G, dv);
-    if (rows <= seg || rows <= kWhole) return 0;
-    // packed: at most rows / seg + B pieces, no fewer than time-major ones
-    return ((size_t)(rows / seg + B) * H * (dk * dv + 1) * 4 + 255) / 256 * 256;
+    if (rows <= kWhole) return 0;
+    // for either form of the batch: packed, at most rows / seg + B pieces, or equal lengths
+    const Fit f(dtype, H, G, dv);
+    const int64_t T = rows / B;
+    int64_t pieces = 0;
+    if (B > 1) {
+        const int seg = ragged_piece(f, rows);
+        if (rows > seg) pieces = rows / seg + B;
+    }
+    if (T > kWhole) {
+        const int seg = even_piece(f, dtype, B, T);
+        if (T > seg) pieces = std::max(pieces, B * ((T + seg - 1) / seg) + (B == 1));
+    }
+    return ((size_t)pieces * H * (dk * dv + 1) * 4 + 255) / 256 * 256;
 }
 
 cudaError_t launch_ssm_prefill(const SsmArgs &a, int dtype, cudaStream_t s) {
     if (token_by_token(a.r)) return launch_ssm_step(a, dtype, s);
-    const int seg = longest(a.r) <= kWhole ? kWhole : piece_tokens(a.r, dtype, a.H, a.G, a.dv);
-    const bool cut = longest(a.r) > seg;
+    const Fit f(dtype, a.H, a.G, a.dv);
+    const int64_t most = longest(a.r);
+    const int seg = most <= kWhole                ? kWhole
+                    : a.r.cu && a.r.B > 1 ? ragged_piece(f, a.r.rows)
+                                          : even_piece(f, dtype, a.r.B, most);
+    const bool cut = most > seg;
     if (dtype == kBF16) return launch_ssm_umma(a, seg, cut, s);
     return launch_ssm_tc(a, dtype, seg, cut, s);
 }
