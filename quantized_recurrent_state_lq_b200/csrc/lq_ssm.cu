@@ -129,10 +129,12 @@ constexpr int kJoin = 8, kJoinThreads = 128;
 // One thread per 4 state elements; block y takes every gridDim.y-th sequence and
 // skips those of one piece, 32 at a time.  kJoin pieces' states are on their way
 // at a time (128 pieces of 2 heads of 64 x 64: 37 us for the prompt, 62 one by one).
-__global__ void __launch_bounds__(kJoinThreads) ssm_join_kernel(SsmArgs a, int seg) {
+__global__ void __launch_bounds__(kJoinThreads) ssm_join_kernel(SsmArgs a, int seg, bool early) {
     const int64_t per = (int64_t)a.dk * a.dv / 4, all = per * a.H;
     const int64_t i = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x;   // (head, element)
     const int lane = threadIdx.x & 31, step = gridDim.y;
+    if (early) let_next_kernel_start();
+    wait_for_kernel_before();
     for (int64_t b0 = blockIdx.y; b0 < a.r.B; b0 += 32 * step) {
         const int64_t bl = b0 + lane * step;
         unsigned todo = __ballot_sync(0xffffffffu, bl < a.r.B && pieces_of(a.r, seg, (int)bl) > 1);
@@ -230,11 +232,11 @@ int64_t longest(const Rows &r) { return r.cu ? r.rows : r.rows / r.B; }
 
 }  // namespace
 
-cudaError_t launch_ssm_join(const SsmArgs &a, int seg, cudaStream_t s) {
+cudaError_t launch_ssm_join(const SsmArgs &a, int seg, bool early, cudaStream_t s) {
     const int64_t n = (int64_t)a.H * a.dk * a.dv / 4, x = (n + kJoinThreads - 1) / kJoinThreads;
     const int64_t y = (4 * 148 + x - 1) / x;   // about four CTAs per SM
-    ssm_join_kernel<<<dim3((unsigned)x, (unsigned)(y < a.r.B ? y : a.r.B)), kJoinThreads, 0, s>>>(a, seg);
-    return cudaGetLastError();
+    return launch_after(ssm_join_kernel, dim3((unsigned)x, (unsigned)(y < a.r.B ? y : a.r.B)), kJoinThreads, 0, s, a,
+                        seg, early);
 }
 
 // Whether a prompt runs token by token.  A chunk costs about as much (7 to 10 us)

@@ -42,9 +42,36 @@ __device__ __forceinline__ long long warp_scan(long long v) {
     return v;
 }
 
+// The join and the scan after it are launched while the kernel before still runs
+// (programmatic dependent launch) and wait until it is done and its results are
+// there: the launches and what comes ahead of the wait are hidden (600 bf16 tokens
+// of two sequences: 24 us against 26).  Nothing that a kernel before writes is read,
+// and nothing that it reads is written, ahead of the wait.
+__device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = dim3((unsigned)threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kernel, P(args)...);
+}
+
 // Chain the pieces of every sequence cut in more than one:  S = S0; for each
 // piece, slot <- S and S <- decay S + own.
-cudaError_t launch_ssm_join(const SsmArgs &a, int seg, cudaStream_t s);
+// early: the scan's CTAs may take their places meanwhile (one per SM; several per SM
+// would pile up on the SMs that are free first, 43 us against 34 for 2048 f32 tokens
+// of 4 heads of 128 x 64).
+cudaError_t launch_ssm_join(const SsmArgs &a, int seg, bool early, cudaStream_t s);
 
 // The chunked scans, with pieces of seg tokens (whole chunks); split: at least
 // one sequence may be cut.

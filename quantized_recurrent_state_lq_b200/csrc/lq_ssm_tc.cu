@@ -123,7 +123,9 @@ __global__ void __launch_bounds__(2 * DV, DV == 128 ? 2 : 4) ssm_tc_kernel(SsmAr
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
     const int z = blockIdx.x / a.H, h = blockIdx.x % a.H;
     Piece p;
-    if (!(FULL ? find_piece(a.r, seg, z, p) : find_cut(a.r, seg, z, p))) return;
+    const bool found = FULL ? find_piece(a.r, seg, z, p) : find_cut(a.r, seg, z, p);
+    if (FULL) wait_for_kernel_before();
+    if (!found) return;
     const int g = (int)((int64_t)h * a.G / a.H);
     const T *xp = static_cast<const T *>(a.x) + (int64_t)h * DV;
     const T *bp = static_cast<const T *>(a.Bm) + g * DK;
@@ -383,8 +385,10 @@ cudaError_t launch(const SsmArgs &a, int seg, int vec, bool cut, cudaStream_t s)
         e = cudaFuncSetAttribute(ssm_tc_kernel<T, DK, DV, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
         ssm_tc_kernel<T, DK, DV, false><<<(unsigned)(cut_count(a.r, seg) * a.H), NT, bytes, s>>>(a, seg, vec, cut);
-        e = launch_ssm_join(a, seg, s);
+        e = launch_ssm_join(a, seg, false, s);
         if (e != cudaSuccess) return e;
+        return launch_after(ssm_tc_kernel<T, DK, DV, true>, dim3((unsigned)(piece_count(a.r, seg) * a.H)), NT, bytes, s, a,
+                            seg, vec, cut);
     }
     ssm_tc_kernel<T, DK, DV, true><<<(unsigned)(piece_count(a.r, seg) * a.H), NT, bytes, s>>>(a, seg, vec, cut);
     return cudaGetLastError();

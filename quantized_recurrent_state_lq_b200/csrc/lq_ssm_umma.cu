@@ -454,6 +454,7 @@ __global__ void __launch_bounds__(kNT, 1)
         if (!mbar_wait_bounded(&fx.bar[bar], parity, nullptr)) fx.bad = 1;
     };
 
+    if (wid == 2) tmem_alloc(&fx.tmem, 512);
     if (finder) {
         if (direct) {
             only_item();
@@ -465,15 +466,15 @@ __global__ void __launch_bounds__(kNT, 1)
             for (int i = 0; i < 8; ++i) mbar_init(&fx.bar[i], 1);
             fx.bad = 0;
             fence_mbar_init();
-            if (fx.item[0].valid) {
-                if (tma) {
-                    load_b(fx.item[0], fx.item[0].t_first);
-                    load_c(fx.item[0], fx.item[0].t_first);
-                }
-                load_state(fx.item[0]);
+            if (fx.item[0].valid && tma) {
+                load_b(fx.item[0], fx.item[0].t_first);
+                load_c(fx.item[0], fx.item[0].t_first);
             }
         }
+        wait_for_kernel_before();
+        if (lane == 0 && fx.item[0].valid) load_state(fx.item[0]);
     }
+    wait_for_kernel_before();
     if (a.r.cu) {   // a sequence without tokens hands its state through
         for (int b = blockIdx.x; b < a.r.B; b += gridDim.x)
             if (seq_len(b) == 0)
@@ -481,7 +482,6 @@ __global__ void __launch_bounds__(kNT, 1)
                     reinterpret_cast<float4 *>(a.S_out + b * sall)[i] =
                         a.S0 ? reinterpret_cast<const float4 *>(a.S0 + b * sall)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    if (wid == 2) tmem_alloc(&fx.tmem, 512);
     if (ti < 256) (&fx.first[0][0])[ti] = Q;
     if (ti < 2) fx.nf[ti] = 0;
     if (DK < 128) {   // B^T has 128 rows: the missing key rows are zero
@@ -926,6 +926,7 @@ __global__ void __launch_bounds__(kNT + 32, 1)
     auto b_tile = [&](int n) { return sm + (n & 1 ? kOffB : kOffC); };
     uint64_t *x_bar = &fx.bar[2], *mma_bar = &fx.bar[3];   // and bar[0], bar[1]: B of even and odd chunks
 
+    let_next_kernel_start();
     if (lead) {
         for (int i = 0; i < 4; ++i) mbar_init(&fx.bar[i], 1);
         fx.bad = 0;
@@ -1142,10 +1143,11 @@ cudaError_t launch(const SsmArgs &a, const SsmMaps &maps, int seg, int tma, int 
         if (e != cudaSuccess) return e;
         const int64_t cuts = cut_count(a.r, seg) * units;
         ssm_state_kernel<DK, HPC><<<grid(cuts), kNT + 32, bytes, s>>>(a, maps, seg, cuts, tma);
-        e = launch_ssm_join(a, seg, s);
+        e = launch_ssm_join(a, seg, true, s);
         if (e != cudaSuccess) return e;
     }
     const int64_t items = piece_count(a.r, seg) * units;
+    if (split) return launch_after(ssm_umma_kernel<DK, HPC>, grid(items), kNT, bytes, s, a, maps, seg, tma, split, items <= kSms);
     ssm_umma_kernel<DK, HPC><<<grid(items), kNT, bytes, s>>>(a, maps, seg, tma, split, items <= kSms);
     return cudaGetLastError();
 }
