@@ -548,6 +548,52 @@ def test_side_stream_and_graph_replay():
         assert all(torch.equal(a, b) for a, b in zip(want, out))
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+def test_cut_prompts_queued_one_after_the_other(dtype):
+    """Prompts cut along their length, queued without a wait: one workspace for
+    all, states in place from call to call, inputs overwritten behind each call;
+    eager and from a graph replayed with other values and other lengths.  The
+    same bits as with a wait after every call."""
+    _gpu()
+    v = _ssm_inputs(17, (1600,), 2, 4, 2, 64, 64, dtype)
+    x = [v["x"] * f for f in (1.0, -0.5, 0.25)]
+    offsets = [_cu([1300, 300]), _cu([20, 1580]), _cu([800, 800])]
+    need = lq.lq_ssm_workspace_bytes(dtype, 2, 4, 2, 64, 64, 1600)
+    assert need > 0
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    xin, cu, S = torch.empty_like(x[0]), offsets[0].clone(), v["S0"].clone()
+    y = [torch.empty_like(x[0]) for _ in range(3)]
+
+    def calls(wait):
+        for k in range(3):
+            xin.copy_(x[k])
+            cu.copy_(offsets[k])
+            lq.lq_ssm_prefill(xin, v["dt"], v["A"], v["Bm"], v["Cm"], D=v["D"], dt_bias=v["dt_bias"], S0=S, S_out=S,
+                              y=y[k], cu=cu, workspace=ws)
+            if wait:
+                torch.cuda.synchronize()
+        xin.fill_(float("nan"))
+        ws.fill_(255)
+
+    calls(True)
+    want = [t.clone() for t in (*y, S)]
+    for run in range(3):
+        S.copy_(v["S0"])
+        if run < 2:
+            calls(False)
+        else:
+            S0 = S.clone()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                calls(False)
+            for _ in range(2):
+                S.copy_(S0)
+                for t in y:
+                    t.fill_(float("nan"))
+                graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(want, (*y, S))), run
+
+
 def test_same_inputs_same_bits():
     _gpu()
     for dtype in TYPES:
