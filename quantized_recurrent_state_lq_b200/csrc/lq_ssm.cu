@@ -25,7 +25,7 @@ __global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(SsmArgs a) {
     constexpr int LR = CW / 4;               // lanes per key row
     constexpr int RG = kStepThreads / LR;    // key rows side by side
     constexpr int NR = DK / RG;              // key rows per thread
-    __shared__ float sB[DK], sC[DK], sx[CW], part[kStepThreads / 32][CW];
+    __shared__ float sB[2][DK], sC[2][DK], sx[2][CW], part[kStepThreads / 32][CW];
     const int tid = threadIdx.x;
     const int slice = blockIdx.x % (DV / CW);
     const int64_t bh = blockIdx.x / (DV / CW);
@@ -49,25 +49,36 @@ __global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(SsmArgs a) {
         S[i] = a.S0 ? *reinterpret_cast<const float4 *>(a.S0 + base + (int64_t)(rg + i * RG) * DV)
                     : make_float4(0.f, 0.f, 0.f, 0.f);
     const float A = a.A[h], Dh = a.D ? a.D[h] : 0.0f, bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
-    for (int t = 0; t < p.len; ++t) {
+    // A token's inputs, on their way while the one before is at work.
+    T rB, rC, rx, rd;
+    auto fetch = [&](int t) {
         const int64_t row = p.row0 + t * p.step;
-        const T *Bm = static_cast<const T *>(a.Bm) + row * a.ldb + g * DK;
-        const T *Cm = static_cast<const T *>(a.Cm) + row * a.ldc + g * DK;
         if (tid < DK) {
-            sB[tid] = to_f<T>(Bm[tid]);
-            sC[tid] = to_f<T>(Cm[tid]);
+            rB = static_cast<const T *>(a.Bm)[row * a.ldb + g * DK + tid];
+            rC = static_cast<const T *>(a.Cm)[row * a.ldc + g * DK + tid];
         }
-        if (tid < CW) sx[tid] = to_f<T>(static_cast<const T *>(a.x)[row * a.ldx + (int64_t)h * DV + slice * CW + tid]);
-        float d = to_f<T>(static_cast<const T *>(a.dt)[row * a.lddt + h]) + bias;
+        if (tid < CW) rx = static_cast<const T *>(a.x)[row * a.ldx + (int64_t)h * DV + slice * CW + tid];
+        rd = static_cast<const T *>(a.dt)[row * a.lddt + h];
+    };
+    if (p.len > 0) fetch(0);
+    for (int t = 0; t < p.len; ++t) {
+        const int o = t & 1;
+        if (tid < DK) {
+            sB[o][tid] = to_f<T>(rB);
+            sC[o][tid] = to_f<T>(rC);
+        }
+        if (tid < CW) sx[o][tid] = to_f<T>(rx);
+        float d = to_f<T>(rd) + bias;
+        if (t + 1 < p.len) fetch(t + 1);
         if (a.softplus) d = softplus_f(d);
         const float keep = expf(d * A);
         __syncthreads();
-        const float4 x = *reinterpret_cast<const float4 *>(sx + col);
+        const float4 x = *reinterpret_cast<const float4 *>(sx[o] + col);
         const float4 dx = make_float4(d * x.x, d * x.y, d * x.z, d * x.w);
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
-            const float bn = sB[rg + i * RG], cn = sC[rg + i * RG];
+            const float bn = sB[o][rg + i * RG], cn = sC[o][rg + i * RG];
             S[i].x = fmaf(bn, dx.x, keep * S[i].x);
             S[i].y = fmaf(bn, dx.y, keep * S[i].y);
             S[i].z = fmaf(bn, dx.z, keep * S[i].z);
@@ -87,12 +98,11 @@ __global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(SsmArgs a) {
         if ((tid & 31) < LR) *reinterpret_cast<float4 *>(&part[tid >> 5][col]) = y;
         __syncthreads();
         if (tid < CW) {
-            float s = Dh * sx[tid];
+            float s = Dh * sx[o][tid];
 #pragma unroll
             for (int w = 0; w < kStepThreads / 32; ++w) s += part[w][tid];
-            static_cast<T *>(a.y)[row * a.ldy + (int64_t)h * DV + slice * CW + tid] = from_f<T>(s);
+            static_cast<T *>(a.y)[(p.row0 + t * p.step) * a.ldy + (int64_t)h * DV + slice * CW + tid] = from_f<T>(s);
         }
-        if (t + 1 < p.len) __syncthreads();   // sx and part are read before the next token's are written
     }
 #pragma unroll
     for (int i = 0; i < NR; ++i) *reinterpret_cast<float4 *>(a.S_out + base + (int64_t)(rg + i * RG) * DV) = S[i];
