@@ -110,8 +110,11 @@ __global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(SsmArgs a) {
 
 template <typename T, int DK, int DV>
 cudaError_t step(const SsmArgs &a, cudaStream_t s) {
+    // One token is bound by its loads: two CTAs of 64 columns per SM, or four times
+    // as many; more tokens by what every CTA does for each: one CTA per SM (16 tokens
+    // of 8 x 16 heads of 128 x 128: 12.5 us against 18.5).
     const int64_t heads = (int64_t)a.r.B * a.H;
-    if (heads * (DV / 64) >= 148 * 2)
+    if (heads * (DV / 64) >= (a.r.rows > a.r.B ? 148 : 148 * 2))
         ssm_step_kernel<T, DK, DV, 64><<<(unsigned)(heads * (DV / 64)), kStepThreads, 0, s>>>(a);
     else
         ssm_step_kernel<T, DK, DV, 16><<<(unsigned)(heads * (DV / 16)), kStepThreads, 0, s>>>(a);
@@ -249,14 +252,17 @@ cudaError_t launch_ssm_join(const SsmArgs &a, int seg, bool early, cudaStream_t 
                         seg, early);
 }
 
-// Whether a prompt runs token by token.  A chunk costs about as much (7 to 10 us)
-// whatever it holds, a token 0.5 us: so do sequences of at most 16 tokens, and
-// packed batches of at most 2 tokens a sequence on average and 512 in all (64
-// single tokens of 32 heads of 128 x 128: 50 us against 155), where one long
-// sequence costs no more than 512 steps.
-bool token_by_token(const Rows &r) {
-    if (!r.cu) return r.rows / r.B <= 16;
-    return r.rows <= 16 || (r.rows <= 2 * (int64_t)r.B && r.rows <= 512);
+// Whether a prompt runs token by token.  A chunk costs about as much (13 us for
+// bf16, 9 for f16, 14 for f32) whatever it holds, a token 0.35 us with fewer CTAs
+// than SMs and 0.6 with more: so do sequences of at most 16 tokens, 24 of few heads
+// (f16 chunks are of 32), and packed batches of at most 2 tokens a sequence on
+// average and 512 in all (64 single tokens of 32 heads of 128 x 128: 50 us against
+// 155), where one long sequence costs no more than 512 steps.
+bool token_by_token(const SsmArgs &a, int dtype) {
+    const Rows &r = a.r;
+    const int most = dtype != kF16 && (int64_t)r.B * a.H * (a.dv / 64) < 148 ? 24 : 16;
+    if (!r.cu) return r.rows / r.B <= most;
+    return r.rows <= most || (r.rows <= 2 * (int64_t)r.B && r.rows <= 512);
 }
 
 size_t ssm_ws_bytes(int dtype, int B, int rows, int H, int G, int dk, int dv) {
@@ -277,7 +283,7 @@ size_t ssm_ws_bytes(int dtype, int B, int rows, int H, int G, int dk, int dv) {
 }
 
 cudaError_t launch_ssm_prefill(const SsmArgs &a, int dtype, cudaStream_t s) {
-    if (token_by_token(a.r)) return launch_ssm_step(a, dtype, s);
+    if (token_by_token(a, dtype)) return launch_ssm_step(a, dtype, s);
     const Fit f(dtype, a.H, a.G, a.dv);
     const int64_t most = longest(a.r);
     const int seg = most <= kWhole                ? kWhole
