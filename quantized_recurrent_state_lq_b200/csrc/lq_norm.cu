@@ -152,10 +152,11 @@ cudaError_t launch(const NormArgs &a, cudaStream_t s) {
 }
 
 // Team and elements per thread by the group's size alone: few enough threads
-// that most of them have work, few enough elements (2 to 8 accesses in flight,
-// up to 64 elements in registers) that small groups do not step through empty
-// ones -- one class of 32 x 16 for all unaligned groups up to 512 took 96 us for
-// 8192 x 16 groups of 47.
+// that most of them have work, few enough elements (up to 64 in registers) that
+// small groups do not step through empty ones.  Without vector accesses the time
+// goes to latency with every warp an SM holds at work, so what counts is the
+// groups in flight: small teams of 4 to 12 elements a thread (16.8 M elements of bf16
+// norm_in, groups of 31: 14 us, 29 with a warp each; 130: 13 and 30; 1025: 13 and 23).
 template <typename T, typename TX, bool IN>
 cudaError_t by_size(const NormArgs &a, cudaStream_t s) {
     const uintptr_t base = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.z) |
@@ -172,12 +173,19 @@ cudaError_t by_size(const NormArgs &a, cudaStream_t s) {
         if (a.D <= 4096) return launch<T, TX, 8, 256, 2, IN>(a, s);
         return launch<T, TX, 8, 512, 4, IN>(a, s);
     }
-    if (a.D <= 16) return launch<T, TX, 1, 8, 2, IN>(a, s);
-    if (a.D <= 64) return launch<T, TX, 1, 32, 2, IN>(a, s);
-    if (a.D <= 128) return launch<T, TX, 1, 32, 4, IN>(a, s);
-    if (a.D <= 256) return launch<T, TX, 1, 128, 2, IN>(a, s);
+    if (a.D <= 16) return launch<T, TX, 1, 4, 4, IN>(a, s);
+    if (a.D <= 32) return launch<T, TX, 1, 8, 4, IN>(a, s);
+    if (a.D <= 48) return launch<T, TX, 1, 8, 6, IN>(a, s);
+    if (a.D <= 64) return launch<T, TX, 1, 16, 4, IN>(a, s);
+    if (a.D <= 96) return launch<T, TX, 1, 16, 6, IN>(a, s);
+    if (a.D <= 128) return launch<T, TX, 1, 16, 8, IN>(a, s);
+    if (a.D <= 192) return launch<T, TX, 1, 32, 6, IN>(a, s);
+    if (a.D <= 256) return launch<T, TX, 1, 32, 8, IN>(a, s);
+    if (a.D <= 384) return launch<T, TX, 1, 32, 12, IN>(a, s);
     if (a.D <= 512) return launch<T, TX, 1, 128, 4, IN>(a, s);
     if (a.D <= 1024) return launch<T, TX, 1, 128, 8, IN>(a, s);
+    if (a.D <= 1536) return launch<T, TX, 1, 256, 6, IN>(a, s);
+    if (a.D <= 2048) return launch<T, TX, 1, 256, 8, IN>(a, s);
     if (a.D <= 4096) return launch<T, TX, 1, 512, 8, IN>(a, s);
     return launch<T, TX, 1, 1024, 16, IN>(a, s);
 }

@@ -445,6 +445,29 @@ def test_norm_out(dtype, xt, rows, G, D):
                f"norm_out {ids(dtype)} {G}x{D} {act} first={first}")
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+def test_norms_of_every_size_class(dtype):
+    """Groups on both sides of every bound at which the team or the elements per
+    thread change, aligned ones and ones whose rows start anywhere."""
+    _gpu()
+    bounds = (4, 8, 16, 32, 48, 64, 96, 128, 192, 256, 384, 512, 1024, 1536, 2048, 4096)
+    for D in sorted({d + k for d in bounds for k in (0, 1)}):
+        for off in (0, 1):
+            g = _gen(2 * D + off)
+            x, res = (_randn(g, (7, D + off), dtype)[:, off:] for _ in range(2))
+            w = 1 + _randn(g, (D,), scale=0.2)
+            y, h = lq.lq_norm_in(x, w, res=res, scale=0.5, eps=1e-5)
+            ry, rh = R.norm_in(x, w, res, 0.5, 1e-5)
+            terms = 0.5 * x.double().abs() + res.double().abs()
+            inv = 1 / torch.sqrt((rh * rh).mean(-1, keepdim=True) + 1e-5)
+            _close(h, rh, R.half_step(dtype) * (1 + 1e-3) * rh.abs() + 2 * R.U * terms + R.tiny(dtype), f"h {D}")
+            _close(y, ry, _norm_tol(ry, ry.abs() + terms * inv * w.double().abs(), dtype, D, None), f"in {D} {off}")
+            a, b = x.unflatten(-1, (1, D)), res.unflatten(-1, (1, D))
+            y = lq.lq_norm_out(a, w, z=b, eps=1e-6)
+            ry = R.norm_out(a, w, b, "silu", False, None, 1.0, 1e-6)
+            _close(y, ry, _norm_tol(ry, 2 * ry.abs(), dtype, D, "silu"), f"out {D} {off}")
+
+
 def test_norms_in_place_and_zero_rows():
     _gpu()
     g = _gen(3)
