@@ -617,6 +617,32 @@ def test_cut_prompts_queued_one_after_the_other(dtype):
         assert all(torch.equal(a, b) for a, b in zip(want, (*y, S))), run
 
 
+def test_two_streams_at_once():
+    """Cut prompts, convolutions, norms and steps queued on two streams at a time,
+    each call with its own workspace: the bits of one after the other."""
+    _gpu()
+    for dtype in (BF16, F32):
+        sets = []
+        for seed in (31, 32):
+            v = _ssm_inputs(seed, (900,), 2, 4, 2, 128, 64, dtype)
+            g = _gen(seed)
+            sets.append((v, _randn(g, (256, 4)), _randn(g, (64,)), _cu([640, 260])))
+
+        def chain(v, w, wn, cu, stream):
+            xs, win = lq.lq_conv_prefill(v["x"].reshape(900, 256), w, cu=cu, stream=stream)
+            y, S = lq.lq_ssm_prefill(xs.view(900, 4, 64), v["dt"], v["A"], v["Bm"], v["Cm"], S0=v["S0"], cu=cu, stream=stream)
+            z = lq.lq_norm_out(y, wn, z=v["x"], stream=stream)
+            s = lq.lq_ssm_step(S, z[:2], v["dt"][:2], v["A"], v["Bm"][:2], v["Cm"][:2], stream=stream)
+            return y, S, z, s, win
+        want = [chain(*a, torch.cuda.current_stream()) for a in sets]
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in sets]
+        for _ in range(5):
+            got = [chain(*a, s) for a, s in zip(sets, streams)]
+            torch.cuda.synchronize()
+            assert all(torch.equal(p, q) for u, o in zip(want, got) for p, q in zip(u, o))
+
+
 def test_same_inputs_same_bits():
     _gpu()
     for dtype in TYPES:
