@@ -81,6 +81,17 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t at, uint64_t bd, uin
         : "memory");
 }
 
+// Thread l of the warp writes tensor-memory lane (taddr.lane + l), columns
+// taddr.col .. taddr.col + 15 (shape 32x32b).
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
 // 128-byte swizzle: 8-row groups 1024 B apart; MN-major operands of more than
 // 64 columns continue a block further.
 __device__ __forceinline__ uint64_t desc_sw(const void *p, uint32_t lbo) {
