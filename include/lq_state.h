@@ -376,7 +376,7 @@ typedef enum { LQ_ACT_NONE = 0, LQ_ACT_SILU = 1, LQ_ACT_SIGMOID = 2 } lq_act;
 
 typedef struct {
     int32_t dtype;   /* lq_dtype of x, y and the window */
-    int32_t B;       /* sequences */
+    int32_t B;       /* sequences (at most 2^30) */
     int32_t C;       /* channels */
     int32_t K;       /* taps */
     int32_t act;     /* LQ_ACT_NONE or LQ_ACT_SILU */

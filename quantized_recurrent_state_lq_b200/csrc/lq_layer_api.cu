@@ -61,7 +61,7 @@ int check_rows(int32_t B, int32_t rows, const int32_t *d_cu) {
 int check_conv(const lq_conv_config *c) {
     if (!c || !is_dtype(c->dtype)) return LQ_ERR_INVALID_ARG;
     if (c->act != LQ_ACT_NONE && c->act != LQ_ACT_SILU) return LQ_ERR_INVALID_ARG;
-    if (c->B < 1 || c->C < 1) return LQ_ERR_SHAPE;
+    if (c->B < 1 || c->B > (1 << 30) || c->C < 1) return LQ_ERR_SHAPE;   // (a sequence's number plus a batch's fits an int)
     if (c->K < 2 || c->K > LQ_CONV_MAX_TAPS || c->C > (1 << 22)) return LQ_ERR_UNSUPPORTED;
     return LQ_OK;
 }
