@@ -385,6 +385,8 @@ cudaError_t launch(const SsmArgs &a, int seg, int vec, bool cut, cudaStream_t s)
         e = cudaFuncSetAttribute(ssm_tc_kernel<T, DK, DV, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
         ssm_tc_kernel<T, DK, DV, false><<<(unsigned)(cut_count(a.r, seg) * a.H), NT, bytes, s>>>(a, seg, vec, cut);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
         e = launch_ssm_join(a, seg, false, s);
         if (e != cudaSuccess) return e;
         return launch_after(ssm_tc_kernel<T, DK, DV, true>, dim3((unsigned)(piece_count(a.r, seg) * a.H)), NT, bytes, s, a,

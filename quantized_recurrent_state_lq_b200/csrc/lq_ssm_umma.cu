@@ -1157,6 +1157,8 @@ cudaError_t launch(const SsmArgs &a, const SsmMaps &maps, int seg, int tma, int 
         if (e != cudaSuccess) return e;
         const int64_t cuts = cut_count(a.r, seg) * units;
         ssm_state_kernel<DK, HPC><<<grid(cuts), kNT + 32, bytes, s>>>(a, maps, seg, cuts, tma);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
         e = launch_ssm_join(a, seg, true, s);
         if (e != cudaSuccess) return e;
     }
