@@ -20,6 +20,7 @@ def test_every_launch_is_followed_by_its_error(path):
         after = text[end + 1:].lstrip()
         line = text.count("\n", 0, m.start()) + 1
         # the next statement (the else branch's launch is a match of its own)
-        assert re.match(r"(else\s+[^;]*<<<|return cudaGetLastError\(\);|e = cudaGetLastError\(\);[\s}]*if \(e [!=]= cudaSuccess\))",
+        assert re.match(r"(else\s+[^;]*<<<|return cudaGetLastError\(\);|e = cudaGetLastError\(\);[\s}]*(if \()?"
+                        r"(const cudaError_t f = [^;]*;\s*return )?e [!=]= cudaSuccess)",
                         after), \
             f"{os.path.basename(path)}:{line}: launch not checked: {after[:60]!r}"
