@@ -21,6 +21,11 @@ __device__ __forceinline__ long long decay_fix(float l) { return __float2ll_rn(l
 __device__ __forceinline__ float decay_f(long long v) {
     return fmaf((float)(unsigned)v, 0x1p-32f, (float)(int)(v >> 32));
 }
+// The same as an integer part and a fraction (to 2^-25), both floats.
+__device__ __forceinline__ void decay_parts(long long v, float &whole, float &fraction) {
+    whole = (float)(int)(v >> 32);
+    fraction = (float)(unsigned)v * 0x1p-32f;
+}
 
 // A token's step d and log2 decay d A: within +-150 (2^-150 is flushed to 0 in
 // FP32, 2^150 is its infinity), so that no difference of sums is inf - inf.  A

@@ -54,8 +54,9 @@ constexpr int kNT = 512;
 constexpr int kBlk = Q * 128;          // bytes of 128 rows of 64 columns
 constexpr int kOffC = 0, kOffB = 2 * kBlk, kOffX = 4 * kBlk, kOffU = 6 * kBlk, kOffF = 12 * kBlk;
 // Decay factors of even and odd chunks, for up to two heads: [Q] sums within the
-// warp, [Q] d, [3][Q] factors for the rows of later warps.
-constexpr int kFac = 5 * Q, kOffFixed = kOffF + 4 * kFac * 4;
+// warp (integer parts, negated), [Q] d, [3][Q] factors for the rows of later warps,
+// [Q] the sums' fractions (negated).
+constexpr int kFac = 6 * Q, kOffFixed = kOffF + 4 * kFac * 4;
 
 // Instruction descriptors, kind::f16 with bf16 operands and FP32 accumulators.
 constexpr uint32_t idesc(int N, int a_mn, int b_mn) {
@@ -507,9 +508,10 @@ __global__ void __launch_bounds__(kNT, 1)
     tc_fence_after();
     const uint32_t tm = fx.tmem, tl = tm + ((uint32_t)warp << 21);   // this warp's lanes: 32 warp
 
-    // Of the chunk at work: 2^ of the decay up to this token within its warp and
-    // within the chunk, the token's weight in the next state, the chunk's decay.
-    float gwf = 0.0f, et = 0.0f, wr = 0.0f, keep = 0.0f;
+    // Of the chunk at work: the log2 decay up to this token within its warp (integer
+    // part and fraction), 2^ of that within the chunk, the token's weight in the next
+    // state, the chunk's decay.
+    float gi = 0.0f, gf = 0.0f, et = 0.0f, wr = 0.0f, keep = 0.0f;
     Steps st;
     int parity = 0, s_parity = 0;
 
@@ -535,7 +537,7 @@ __global__ void __launch_bounds__(kNT, 1)
                 total += s;
             }
             const long long gt = base + st.gw;
-            gwf = decay_f(st.gw);
+            decay_parts(st.gw, gi, gf);
             et = ex2_f(decay_f(gt));
             wr = st.d * exp2f(decay_f(total - gt));
             keep = exp2f(decay_f(total));
@@ -543,8 +545,9 @@ __global__ void __launch_bounds__(kNT, 1)
             float *fl = reinterpret_cast<float *>(sm + kOffF) + (odd * 2 + hh) * kFac;
             const int part = HPC == 2 ? cq & 1 : cq;
             if (part == 0) {
-                fl[r] = gwf;
+                fl[r] = -gi;
                 fl[Q + r] = st.d;
+                fl[5 * Q + r] = -gf;
             }
             long long end = 0;   // 2^(sum to the end of tokens 32 w .. - g_s) d_s for the rows of later warps
 #pragma unroll
@@ -685,10 +688,13 @@ __global__ void __launch_bounds__(kNT, 1)
             {
                 // M from G, 16 tokens at a time: 8 columns of first parts, 8 of second.
                 // Tokens of earlier warps factor through the boundary before this
-                // warp's, those after this one are zero.
+                // warp's, those after this one are zero.  Within the warp the sums may be
+                // large where their difference is small (31 tokens that wipe the state: 4650):
+                // subtracted in two parts, the difference is good to 2^-24 (in one float
+                // 2^-12 there, which showed in outputs whose terms cancel).
                 const float *fl = reinterpret_cast<const float *>(sm + kOffF) + (odd * 2 + hh) * kFac;
                 const uint32_t to = HPC == 1 ? tl : tl + (hh == 0 ? 384 : 256);
-                const float rf = ex2_f(gwf);
+                const float rf = ex2_f(gi + gf);
                 for (int q = HPC == 2 ? cq & 1 : cq; q < 8; q += HPC == 2 ? 2 : 4) {
                     uint32_t v[16];
                     if (q > 2 * warp + 1) {
@@ -716,21 +722,23 @@ __global__ void __launch_bounds__(kNT, 1)
                         } else {
                             const float4 *gs = reinterpret_cast<const float4 *>(fl + 16 * q);
                             const float4 *ds = reinterpret_cast<const float4 *>(fl + Q + 16 * q);
+                            const float4 *fs = reinterpret_cast<const float4 *>(fl + 5 * Q + 16 * q);
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                const float4 gv = gs[i], dv = ds[i];
-                                const float ge[4] = {gv.x, gv.y, gv.z, gv.w}, de[4] = {dv.x, dv.y, dv.z, dv.w};
-                                float m[4];
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    const float e = ex2_f(gwf - ge[k]) * de[k] * __uint_as_float(v[4 * i + k]);
-                                    m[k] = 16 * (q & 1) + 4 * i + k <= lane ? e : 0.0f;
-                                }
+                                const float4 gv = gs[i], dv = ds[i], fv = fs[i];
+                                const float2 ge[2] = {f2(gv.x, gv.y), f2(gv.z, gv.w)}, de[2] = {f2(dv.x, dv.y), f2(dv.z, dv.w)};
+                                const float2 fe[2] = {f2(fv.x, fv.y), f2(fv.z, fv.w)};
 #pragma unroll
                                 for (int k = 0; k < 2; ++k) {
-                                    float2 mm = f2(m[2 * k], m[2 * k + 1]);
-                                    hi[2 * i + k] = take_part(mm);
-                                    lo[2 * i + k] = last_part(mm);
+                                    const float2 l = __fadd2_rn(__fadd2_rn(f2(gi, gi), ge[k]), __fadd2_rn(f2(gf, gf), fe[k]));
+                                    const float2 gg = f2(__uint_as_float(v[4 * i + 2 * k]),
+                                                         __uint_as_float(v[4 * i + 2 * k + 1]));
+                                    float2 m = mul2(mul2(f2(ex2_f(l.x), ex2_f(l.y)), de[k]), gg);
+                                    const int s = 16 * (q & 1) + 4 * i + 2 * k;
+                                    if (s > lane) m.x = 0.0f;
+                                    if (s + 1 > lane) m.y = 0.0f;
+                                    hi[2 * i + k] = take_part(m);
+                                    lo[2 * i + k] = last_part(m);
                                 }
                             }
                         }
