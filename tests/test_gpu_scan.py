@@ -3,7 +3,9 @@ wrong, against its definition in 64 bits; tolerances as in test_gpu_layer."""
 import pytest
 import torch
 
-from tests.test_gpu_layer import TYPES, _check_ssm, _cu, _gpu, ids
+from quantized_recurrent_state_lq_b200 import lq
+from tests import layer_ref as R
+from tests.test_gpu_layer import BF16, F16, TYPES, _check_ssm, _close, _cu, _gpu, _ssm_inputs, _ssm_tol, ids
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +35,61 @@ def test_slow_tokens_after_wiping_ones(dtype):
     _gpu()
     v, lens = slow_tokens_after_wiping_ones(dtype, "cuda")
     _check_ssm(v, _cu(lens), f"ssm slow after wiping {ids(dtype)}", softplus=False)
+
+
+def _is_cut(v, B, rows):
+    H, dv = v["x"].shape[-2:]
+    G, dk = v["Bm"].shape[-2:]
+    return lq.lq_ssm_workspace_bytes(v["x"].dtype, B, H, G, dk, dv, rows) > 0
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("H,G,dk,dv", [(3, 1, 64, 64), (6, 2, 128, 64), (2, 1, 64, 128), (3, 3, 128, 128)])
+@pytest.mark.parametrize("pad", [8, 1], ids=["aligned", "odd_base"])
+def test_one_packed_prompt_cut(dtype, H, G, dk, dv, pad):
+    """One prompt of 1500 tokens, cut along its length; odd_base: rows that no
+    tensor copy takes.  Odd numbers of 64-column heads a group among them."""
+    _gpu()
+    v = _ssm_inputs(50 + H + pad, (1500,), 1, H, G, dk, dv, dtype, pad=pad)
+    assert (v["x"].data_ptr() % 16 == 0) == (pad == 8)
+    assert _is_cut(v, 1, 1500)
+    _check_ssm(v, _cu([1500]), f"ssm cut {ids(dtype)} H{H} G{G} {dk}x{dv} pad {pad}")
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("H,G,dk,dv,pad", [(3, 1, 64, 64, 8), (2, 2, 128, 64, 8), (2, 1, 128, 128, 8), (1, 1, 64, 128, 1)])
+def test_time_major_prompts_cut(dtype, H, G, dk, dv, pad):
+    """Two sequences of 1100 tokens, row t * 2 + b, cut along their length."""
+    _gpu()
+    v = _ssm_inputs(60 + H + dv, (1100, 2), 2, H, G, dk, dv, dtype, pad=pad)
+    assert _is_cut(v, 2, 2200)
+    _check_ssm(v, None, f"ssm time-major cut {ids(dtype)} H{H} G{G} {dk}x{dv} pad {pad}")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=ids)
+@pytest.mark.parametrize("H,G,dk,dv,pad", [(8, 2, 64, 64, 8), (5, 1, 128, 128, 8), (9, 3, 64, 64, 1)])
+def test_time_major_more_items_than_ctas(dtype, H, G, dk, dv, pad):
+    """40 sequences of 200 tokens, uncut: each CTA walks its share of them."""
+    _gpu()
+    v = _ssm_inputs(70 + H, (200, 40), 40, H, G, dk, dv, dtype, pad=pad)
+    _check_ssm(v, None, f"ssm time-major walk {ids(dtype)} H{H} G{G} {dk}x{dv} pad {pad}")
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+def test_packed_prompts_cut_in_some_sequences_at_odd_bases(dtype):
+    """Sequences of 1300, 0, 37 and 700 tokens behind rows that belong to none,
+    no row on a 16-byte boundary, an odd number of 64-column heads."""
+    _gpu()
+    v = _ssm_inputs(81, (2050,), 4, 3, 1, 128, 64, dtype, pad=3)
+    cu = torch.tensor([9, 1309, 1309, 1346, 2046], dtype=torch.int32, device="cuda")
+    assert _is_cut(v, 4, 2050)
+    inner = {k: (w[9:2046] if k in ("x", "dt", "Bm", "Cm") else w) for k, w in v.items()}
+    y = torch.full((2050, 3, 64), 7.0, dtype=dtype, device="cuda")
+    got, S = lq.lq_ssm_prefill(v["x"], v["dt"], v["A"], v["Bm"], v["Cm"], D=v["D"], dt_bias=v["dt_bias"], S0=v["S0"],
+                               cu=cu, y=y)
+    want, rS, my, mS, n = R.ssm(inner["x"], v["dt"][9:2046], v["A"], inner["Bm"], inner["Cm"], v["D"], v["dt_bias"], True,
+                                v["S0"], cu - 9)
+    ty, tS = _ssm_tol(want, rS, my, mS, n, dtype, 128)
+    assert (got[:9] == 7).all() and (got[2046:] == 7).all()
+    _close(got[9:2046], want, ty, f"ssm cut at odd bases {ids(dtype)} y")
+    _close(S, rS, tS, f"ssm cut at odd bases {ids(dtype)} S")
