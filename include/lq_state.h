@@ -426,7 +426,9 @@ size_t lq_ssm_workspace_bytes(const lq_ssm_config *cfg, int32_t rows);
  * there (beyond, FP32 has 0 and infinity).  A value of x, Bm, Cm or dt that is not
  * finite shows in the outputs and states it reaches and in no earlier token; where
  * it reaches a state's column or row, those entries are not finite (NaN or
- * infinite).  A call gives the same bits every time.
+ * infinite).  A call gives the same bits every time.  Every wait inside has a time
+ * limit; one that runs out leaves NaN, never a value that looks like a result, in
+ * the outputs and states that depend on it (lq_selftest_ssm_wait).
  * d_ws: caller-owned device workspace of at least lq_ssm_workspace_bytes(cfg, rows)
  * bytes, 256-byte aligned (else LQ_ERR_WORKSPACE; NULL when that is 0), used by
  * this call until it completes on `stream`: calls that may overlap need a
@@ -438,7 +440,23 @@ int lq_ssm_prefill(const lq_ssm_config *cfg, int32_t rows, const int32_t *d_cu, 
                    int64_t ldc, const float *d_D, const float *d_dt_bias, const float *d_S0, float *d_S_out, void *d_y,
                    int64_t ldy, void *d_ws, size_t ws_bytes, void *stream);
 
-/* The same for one token of each sequence (rows [B, ...]); the states d_S
+/*
+ * Self-test of failure detection: lq_ssm_prefill for bf16 (else
+ * LQ_ERR_UNSUPPORTED) in which a wait counts as run out, although it was not, in
+ * every CTA that takes a sequence, or a piece of one that is cut, whose first row
+ * is `row` (before its first chunk) or whose last row it is (after its last).
+ * 0 <= row < rows, else LQ_ERR_INVALID_ARG.  What that CTA takes from there on is
+ * NaN, with the states and the later pieces behind it; all else is what
+ * lq_ssm_prefill gives.  No effect on any other row, or on prompts that run token
+ * by token.
+ */
+int lq_selftest_ssm_wait(const lq_ssm_config *cfg, int32_t rows, const int32_t *d_cu, const void *d_x, int64_t ldx,
+                         const void *d_dt, int64_t lddt, const float *d_A, const void *d_Bm, int64_t ldb,
+                         const void *d_Cm, int64_t ldc, const float *d_D, const float *d_dt_bias, const float *d_S0,
+                         float *d_S_out, void *d_y, int64_t ldy, void *d_ws, size_t ws_bytes, int32_t row,
+                         void *stream);
+
+/* lq_ssm_prefill for one token of each sequence (rows [B, ...]); the states d_S
  * [B,H,dk,dv] are updated in place.  No workspace. */
 int lq_ssm_step(const lq_ssm_config *cfg, float *d_S, const void *d_x, int64_t ldx, const void *d_dt, int64_t lddt,
                 const float *d_A, const void *d_Bm, int64_t ldb, const void *d_Cm, int64_t ldc, const float *d_D,

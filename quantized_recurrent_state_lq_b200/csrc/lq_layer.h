@@ -41,6 +41,7 @@ struct SsmArgs {
     void *y;
     int64_t ldy;
     float *ws;                      // segment states and decays (ssm_ws_bytes)
+    int64_t fail_row;               // self-test: a wait of the piece that starts or ends at this row counts as run out (-1: none)
 };
 
 struct NormArgs {

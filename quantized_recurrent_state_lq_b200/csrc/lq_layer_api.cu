@@ -81,6 +81,7 @@ lq::SsmArgs ssm_args(const lq_ssm_config *c, int32_t rows, const int32_t *d_cu) 
     a.r.rows = rows;
     a.H = c->H; a.G = c->G; a.dk = c->dk; a.dv = c->dv;
     a.softplus = c->softplus;
+    a.fail_row = -1;
     return a;
 }
 
@@ -162,6 +163,40 @@ lq::NormArgs norm_args(const lq_norm_config *c, const void *x, int64_t ldx, cons
     return a;
 }
 
+int ssm_prefill(const lq_ssm_config *cfg, int32_t rows, const int32_t *d_cu, const void *d_x, int64_t ldx,
+                const void *d_dt, int64_t lddt, const float *d_A, const void *d_Bm, int64_t ldb, const void *d_Cm,
+                int64_t ldc, const float *d_D, const float *d_dt_bias, const float *d_S0, float *d_S_out, void *d_y,
+                int64_t ldy, void *d_ws, size_t ws_bytes, int64_t fail_row, void *stream) {
+    int rc = check_ssm(cfg);
+    if (!rc) rc = check_rows(cfg->B, rows, d_cu);
+    if (rc) return rc;
+    lq::SsmArgs a = ssm_args(cfg, rows, d_cu);
+    a.x = d_x; a.ldx = ldx; a.dt = d_dt; a.lddt = lddt;
+    a.Bm = d_Bm; a.ldb = ldb; a.Cm = d_Cm; a.ldc = ldc;
+    a.A = d_A; a.D = d_D; a.dt_bias = d_dt_bias;
+    a.S0 = d_S0; a.S_out = d_S_out; a.y = d_y; a.ldy = ldy;
+    a.fail_row = fail_row;
+    rc = check_ssm_arrays(cfg, a);
+    if (rc) return rc;
+    const size_t need = lq_ssm_workspace_bytes(cfg, rows);
+    if (need > 0) {
+        if (!d_ws || misaligned(d_ws, 256) || ws_bytes < need) return LQ_ERR_WORKSPACE;
+        const int e = size_of(cfg->dtype);
+        const int64_t wx = (int64_t)cfg->H * cfg->dv, wb = (int64_t)cfg->G * cfg->dk;
+        const int64_t sb = (int64_t)cfg->B * cfg->H * cfg->dk * cfg->dv * 4;
+        const Span ws = flat(d_ws, (int64_t)need);
+        const Span other[] = {rows_of(d_x, rows, wx, ldx, e),  rows_of(d_dt, rows, cfg->H, lddt, e),
+                           rows_of(d_Bm, rows, wb, ldb, e), rows_of(d_Cm, rows, wb, ldc, e),
+                           rows_of(d_y, rows, wx, ldy, e),  flat(d_S0, sb), flat(d_S_out, sb),
+                           flat(d_A, (int64_t)cfg->H * 4),  flat(d_D, (int64_t)cfg->H * 4),
+                           flat(d_dt_bias, (int64_t)cfg->H * 4), offsets(a.r)};
+        for (const Span &o : other)
+            if (overlap(ws, o)) return LQ_ERR_INVALID_ARG;
+        a.ws = static_cast<float *>(d_ws);
+    }
+    return rc_of(lq::launch_ssm_prefill(a, cfg->dtype, static_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -228,33 +263,19 @@ int lq_ssm_prefill(const lq_ssm_config *cfg, int32_t rows, const int32_t *d_cu, 
                    const void *d_dt, int64_t lddt, const float *d_A, const void *d_Bm, int64_t ldb, const void *d_Cm,
                    int64_t ldc, const float *d_D, const float *d_dt_bias, const float *d_S0, float *d_S_out, void *d_y,
                    int64_t ldy, void *d_ws, size_t ws_bytes, void *stream) {
-    int rc = check_ssm(cfg);
-    if (!rc) rc = check_rows(cfg->B, rows, d_cu);
-    if (rc) return rc;
-    lq::SsmArgs a = ssm_args(cfg, rows, d_cu);
-    a.x = d_x; a.ldx = ldx; a.dt = d_dt; a.lddt = lddt;
-    a.Bm = d_Bm; a.ldb = ldb; a.Cm = d_Cm; a.ldc = ldc;
-    a.A = d_A; a.D = d_D; a.dt_bias = d_dt_bias;
-    a.S0 = d_S0; a.S_out = d_S_out; a.y = d_y; a.ldy = ldy;
-    rc = check_ssm_arrays(cfg, a);
-    if (rc) return rc;
-    const size_t need = lq_ssm_workspace_bytes(cfg, rows);
-    if (need > 0) {
-        if (!d_ws || misaligned(d_ws, 256) || ws_bytes < need) return LQ_ERR_WORKSPACE;
-        const int e = size_of(cfg->dtype);
-        const int64_t wx = (int64_t)cfg->H * cfg->dv, wb = (int64_t)cfg->G * cfg->dk;
-        const int64_t sb = (int64_t)cfg->B * cfg->H * cfg->dk * cfg->dv * 4;
-        const Span ws = flat(d_ws, (int64_t)need);
-        const Span other[] = {rows_of(d_x, rows, wx, ldx, e),  rows_of(d_dt, rows, cfg->H, lddt, e),
-                              rows_of(d_Bm, rows, wb, ldb, e), rows_of(d_Cm, rows, wb, ldc, e),
-                              rows_of(d_y, rows, wx, ldy, e),  flat(d_S0, sb), flat(d_S_out, sb),
-                              flat(d_A, (int64_t)cfg->H * 4),  flat(d_D, (int64_t)cfg->H * 4),
-                              flat(d_dt_bias, (int64_t)cfg->H * 4), offsets(a.r)};
-        for (const Span &o : other)
-            if (overlap(ws, o)) return LQ_ERR_INVALID_ARG;
-        a.ws = static_cast<float *>(d_ws);
-    }
-    return rc_of(lq::launch_ssm_prefill(a, cfg->dtype, static_cast<cudaStream_t>(stream)));
+    return ssm_prefill(cfg, rows, d_cu, d_x, ldx, d_dt, lddt, d_A, d_Bm, ldb, d_Cm, ldc, d_D, d_dt_bias, d_S0, d_S_out,
+                       d_y, ldy, d_ws, ws_bytes, -1, stream);
+}
+
+int lq_selftest_ssm_wait(const lq_ssm_config *cfg, int32_t rows, const int32_t *d_cu, const void *d_x, int64_t ldx,
+                         const void *d_dt, int64_t lddt, const float *d_A, const void *d_Bm, int64_t ldb,
+                         const void *d_Cm, int64_t ldc, const float *d_D, const float *d_dt_bias, const float *d_S0,
+                         float *d_S_out, void *d_y, int64_t ldy, void *d_ws, size_t ws_bytes, int32_t row,
+                         void *stream) {
+    if (row < 0 || row >= rows) return LQ_ERR_INVALID_ARG;
+    if (cfg && cfg->dtype != LQ_BF16) return LQ_ERR_UNSUPPORTED;
+    return ssm_prefill(cfg, rows, d_cu, d_x, ldx, d_dt, lddt, d_A, d_Bm, ldb, d_Cm, ldc, d_D, d_dt_bias, d_S0, d_S_out,
+                       d_y, ldy, d_ws, ws_bytes, row, stream);
 }
 
 int lq_ssm_step(const lq_ssm_config *cfg, float *d_S, const void *d_x, int64_t ldx, const void *d_dt, int64_t lddt,

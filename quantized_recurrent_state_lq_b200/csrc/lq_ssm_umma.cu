@@ -298,11 +298,84 @@ struct Steps {
     }
 };
 
+// Tokens of sequence b.
+__device__ __forceinline__ int seq_len(const Rows &r, int b) {
+    return r.cu ? max(cu_at(r, b + 1) - cu_at(r, b), 0) : r.rows / r.B;
+}
+
+__device__ __forceinline__ void place(const SsmArgs &a, int seg, Item &it) {
+    it.t_first = it.p.j * seg;
+    it.t_end = min(it.p.len, it.t_first + seg);
+    it.tm_t = a.r.cu ? (int)it.p.row0 : 0;
+    it.tm_b = a.r.cu ? 0 : it.p.b;
+}
+
+// The next item of the CTA's share (by one warp).
+template <int HPC>
+__device__ __forceinline__ void next_item(const SsmArgs &a, int seg, Fixed &fx, Item &out) {
+    const int units = unit_count<HPC>(a.H, a.G);
+    Walk w = fx.walk;
+    Item it;
+    it.valid = false;
+    while (w.pos < w.end && w.b < a.r.B && !it.valid) {
+        const int c0 = a.r.cu ? cu_at(a.r, w.b) : 0, len = seq_len(a.r, w.b), n = (len + seg - 1) / seg;
+        if (w.u >= units) {
+            w.u = 0;
+            ++w.j;
+        }
+        if (w.j >= n) {
+            w.j = w.u = 0;
+            ++w.b;
+            continue;
+        }
+        it.valid = true;
+        it.p.b = w.b;
+        it.p.j = w.j;
+        it.p.len = len;
+        it.p.n = n;
+        it.p.row0 = a.r.cu ? c0 : w.b;
+        it.p.step = a.r.cu ? 1 : a.r.B;
+        it.p.id = (a.r.cu ? c0 / seg + w.b : (int64_t)w.b * n) + w.j;
+        it.u = unit_of<HPC>(w.u++, a.H, a.G);
+        place(a, seg, it);
+        w.pos += (it.t_end - it.t_first + Q - 1) / Q;
+    }
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+        out = it;
+        fx.walk = w;
+    }
+    __syncwarp();
+}
+
+// After a wait that ran out: NaN for the outputs and the final state of the item at
+// work, item[sel], and of all that this CTA would have taken after it (item[sel ^ 1]
+// holds the next one if `known`).  By the whole CTA; apart from the kernel, whose
+// registers it would cost.
+template <int DK, int HPC>
+__device__ __noinline__ void leave_nan(const SsmArgs &a, int seg, Fixed &fx, int sel, bool known) {
+    constexpr int DV = 128 / HPC;
+    for (;; sel ^= 1, known = false) {
+        const Item &it = fx.item[sel];
+        const int width = it.u.heads * DV;
+        for (int i = threadIdx.x; i < (it.t_end - it.t_first) * width; i += kNT) {
+            const int64_t row = it.p.row0 + (int64_t)(it.t_first + i / width) * it.p.step;
+            static_cast<uint16_t *>(a.y)[row * a.ldy + it.u.h * DV + i % width] = 0x7fff;
+        }
+        if (it.p.j == it.p.n - 1)
+            for (int i = threadIdx.x; i < it.u.heads * DK * DV; i += kNT)
+                a.S_out[((int64_t)it.p.b * a.H + it.u.h) * DK * DV + i] = __int_as_float(0x7fffffff);
+        if (!known && threadIdx.x < 32) next_item<HPC>(a, seg, fx, fx.item[sel ^ 1]);
+        __syncthreads();
+        if (!fx.item[sel ^ 1].valid) return;
+    }
+}
+
 // Outputs and final states.  Each CTA walks its share of the items; its second
 // warp finds the next one and sends for its first tiles before the last one ends.
 template <int DK, int HPC>
 __global__ void __launch_bounds__(kNT, 1)
-    ssm_umma_kernel(SsmArgs a, const __grid_constant__ SsmMaps maps, int seg, int tma, int split,
+    ssm_umma_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ SsmMaps maps, int seg, int tma, int split,
                     int direct) {
     constexpr int DV = 128 / HPC;
     // Tensor memory: G at 0, Y with C S's first part at 128, its second at 256.
@@ -321,13 +394,10 @@ __global__ void __launch_bounds__(kNT, 1)
     const int64_t sall = (int64_t)a.H * DK * DV;
 
     float S[CW];   // the state's key row r, this thread's columns
-    auto seq_len = [&](int b) {
-        return a.r.cu ? max(cu_at(a.r, b + 1) - cu_at(a.r, b), 0) : a.r.rows / a.r.B;
-    };
     // (Both by the second warp.)  The first item that starts in this CTA's part.
     auto start_walk = [&]() {
         Walk w{};
-        auto seq_chunks = [&](int b) { return b < a.r.B ? (seq_len(b) + Q - 1) / Q : 0; };
+        auto seq_chunks = [&](int b) { return b < a.r.B ? (seq_len(a.r, b) + Q - 1) / Q : 0; };
         int64_t before = 0;   // chunks of the sequences before b
         w.b = a.r.B;
         if (!a.r.cu) {
@@ -369,7 +439,7 @@ __global__ void __launch_bounds__(kNT, 1)
             }
         }
         if (w.b < a.r.B) {
-            const int len = seq_len(w.b), n = (len + seg - 1) / seg, whole = seg / Q;
+            const int len = seq_len(a.r, w.b), n = (len + seg - 1) / seg, whole = seg / Q;
             const int64_t o = w.pos - before, per = (int64_t)whole * units;
             w.j = (int)min(o / per, (int64_t)(n - 1));
             const int c = w.j < n - 1 ? whole : ((len - w.j * seg) + Q - 1) / Q;
@@ -379,56 +449,16 @@ __global__ void __launch_bounds__(kNT, 1)
         if (lane == 0) fx.walk = w;
         __syncwarp();
     };
-    auto place = [&](Item &it) {
-        it.t_first = it.p.j * seg;
-        it.t_end = min(it.p.len, it.t_first + seg);
-        it.tm_t = a.r.cu ? (int)it.p.row0 : 0;
-        it.tm_b = a.r.cu ? 0 : it.p.b;
-    };
     // No more items than CTAs: this one's is found without the walk (3000 cycles).
     auto only_item = [&]() {
         const int z = (int)(blockIdx.x / (unsigned)units);
         Item it;
         it.valid = find_piece(a.r, seg, z, it.p) && it.p.len > 0;
         it.u = unit_of<HPC>((int)(blockIdx.x - (unsigned)z * units), a.H, a.G);
-        place(it);
+        place(a, seg, it);
         if (lane == 0) {
             fx.item[0] = it;
             fx.walk = Walk{};
-        }
-        __syncwarp();
-    };
-    auto next_item = [&](Item &out) {
-        Walk w = fx.walk;
-        Item it;
-        it.valid = false;
-        while (w.pos < w.end && w.b < a.r.B && !it.valid) {
-            const int c0 = a.r.cu ? cu_at(a.r, w.b) : 0, len = seq_len(w.b), n = (len + seg - 1) / seg;
-            if (w.u >= units) {
-                w.u = 0;
-                ++w.j;
-            }
-            if (w.j >= n) {
-                w.j = w.u = 0;
-                ++w.b;
-                continue;
-            }
-            it.valid = true;
-            it.p.b = w.b;
-            it.p.j = w.j;
-            it.p.len = len;
-            it.p.n = n;
-            it.p.row0 = a.r.cu ? c0 : w.b;
-            it.p.step = a.r.cu ? 1 : a.r.B;
-            it.p.id = (a.r.cu ? c0 / seg + w.b : (int64_t)w.b * n) + w.j;
-            it.u = unit_of<HPC>(w.u++, a.H, a.G);
-            place(it);
-            w.pos += (it.t_end - it.t_first + Q - 1) / Q;
-        }
-        __syncwarp();
-        if (lane == 0) {
-            out = it;
-            fx.walk = w;
         }
         __syncwarp();
     };
@@ -475,7 +505,7 @@ __global__ void __launch_bounds__(kNT, 1)
             only_item();
         } else {
             start_walk();
-            next_item(fx.item[0]);
+            next_item<HPC>(a, seg, fx, fx.item[0]);
         }
         if (lane == 0) {
             for (int i = 0; i < 8; ++i) mbar_init(&fx.bar[i], 1);
@@ -492,7 +522,7 @@ __global__ void __launch_bounds__(kNT, 1)
     wait_for_kernel_before();
     if (a.r.cu) {   // a sequence without tokens hands its state through
         for (int b = blockIdx.x; b < a.r.B; b += gridDim.x)
-            if (seq_len(b) == 0)
+            if (seq_len(a.r, b) == 0)
                 for (int64_t i = ti; i < sall / 4; i += kNT)
                     reinterpret_cast<float4 *>(a.S_out + b * sall)[i] =
                         a.S0 ? reinterpret_cast<const float4 *>(a.S0 + b * sall)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -515,7 +545,9 @@ __global__ void __launch_bounds__(kNT, 1)
     Steps st;
     int parity = 0, s_parity = 0;
 
-    for (int sel = 0; fx.item[sel].valid; sel ^= 1) {
+    int sel = 0;
+    bool known = false;
+    for (; fx.item[sel].valid; sel ^= 1) {
         const Item &it = fx.item[sel];
         const Piece &p = it.p;
         const int t_end = it.t_end;
@@ -579,6 +611,7 @@ __global__ void __launch_bounds__(kNT, 1)
             wait(kBarS0, s_parity);
             s_parity ^= 1;
         }
+        if (lead && p.row0 + it.t_first * p.step == a.fail_row) fx.bad = 1;
 #pragma unroll
         for (int i = 0; i < CW / 4; ++i) {
             const uint4 z = make_uint4(0u, 0u, 0u, 0u), v = given && r < DK && active ? *chunk(s_in(cq), r, i) : z;
@@ -595,7 +628,8 @@ __global__ void __launch_bounds__(kNT, 1)
         }
         finish(0);
         scan(raw1, it.t_first + Q + r, 1);
-        for (int t0 = it.t_first; t0 < t_end; t0 += Q, parity ^= 1) {
+        int t0 = it.t_first;
+        for (; t0 < t_end; t0 += Q, parity ^= 1) {
             const bool tail = t0 + Q > p.len, last = t0 + Q >= t_end;
             const int odd = ((t0 - it.t_first) / Q) & 1;
             fence_async_smem();
@@ -821,7 +855,7 @@ __global__ void __launch_bounds__(kNT, 1)
                 finish(odd ^ 1);
                 scan(raw, t0 + 2 * Q + r, odd);
             } else if (finder) {
-                next_item(fx.item[sel ^ 1]);
+                next_item<HPC>(a, seg, fx, fx.item[sel ^ 1]);
             }
             // outputs into X's place, then whole rows of 256 bytes at a time
             wait(kBarY, parity);
@@ -891,21 +925,26 @@ __global__ void __launch_bounds__(kNT, 1)
             }
             if (!last) split_state();
         }
-        // The last piece's state leaves; one after a wait that ran out does not look
-        // like a state.
+        // The last piece's state leaves.
         const bool ends = p.j == p.n - 1;
         if (ends && r < DK) {
-            const bool bad = fx.bad;
 #pragma unroll
-            for (int i = 0; i < CW / 4; ++i) {
-                uint32_t v[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] = bad ? 0x7fffffffu : __float_as_uint(S[4 * i + k]);
-                *chunk(sm + kOffU + cq * kBlk, r, i) = make_uint4(v[0], v[1], v[2], v[3]);
-            }
+            for (int i = 0; i < CW / 4; ++i)
+                *chunk(sm + kOffU + cq * kBlk, r, i) =
+                    make_uint4(__float_as_uint(S[4 * i]), __float_as_uint(S[4 * i + 1]), __float_as_uint(S[4 * i + 2]),
+                               __float_as_uint(S[4 * i + 3]));
         }
+        if (lead && p.row0 + (t_end - 1) * p.step == a.fail_row) fx.bad = 1;
         fence_async_smem();
         __syncthreads();   // (and the next item is known)
+        if (fx.bad) {
+            known = t0 >= t_end;
+            if (known && lead_x && tma && fx.item[sel ^ 1].valid) {   // the next item's copies under way
+                wait(kBarB, parity);
+                wait(kBarC, parity);
+            }
+            break;
+        }
         if (finder && lane == 0) {
             if (ends) {
                 const int64_t head = (int64_t)p.b * a.H + it.u.h;
@@ -913,13 +952,13 @@ __global__ void __launch_bounds__(kNT, 1)
                     tma_store_state(&maps.s_out, sm + kOffU + c * kBlk, c * CW % DV, (int)((head + c * CW / DV) * DK));
                 asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             }
-            if (!fx.bad && fx.item[sel ^ 1].valid) load_state(fx.item[sel ^ 1]);
+            if (fx.item[sel ^ 1].valid) load_state(fx.item[sel ^ 1]);
             asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         }
         __syncwarp();
-        if (fx.bad) break;
     }
     if (finder && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (fx.bad) leave_nan<DK, HPC>(a, seg, fx, sel, known);
     tc_fence_before();
     __syncthreads();
     if (wid == 2) {
@@ -929,14 +968,14 @@ __global__ void __launch_bounds__(kNT, 1)
 }
 
 // The pieces' own states, from zero, and their decays, for every piece that is
-// followed by another (all of them seg tokens long): only B^T X' and the state
-// update.  Without C and S the tiles of B have two places, a chunk ahead, and
-// the products of a chunk two accumulators, so that the update runs beside the
-// next chunk's MMAs; a 17th warp issues the copies and the MMAs.
+// followed by another (all of them seg tokens long), one unit of one piece a CTA:
+// only B^T X' and the state update.  Without C and S the tiles of B have two places,
+// a chunk ahead, and the products of a chunk two accumulators, so that the update
+// runs beside the next chunk's MMAs; a 17th warp issues the copies and the MMAs.
 //   [0, 32K) B of even chunks, [32K, 64K) of odd ones, [64K, 96K) X, [96K, 192K) X' parts
 template <int DK, int HPC>
 __global__ void __launch_bounds__(kNT + 32, 1)
-    ssm_state_kernel(SsmArgs a, const __grid_constant__ SsmMaps maps, int seg, int64_t items, int tma) {
+    ssm_state_kernel(SsmArgs a, const __grid_constant__ SsmMaps maps, int seg, int tma) {
     constexpr int DV = 128 / HPC;
     extern __shared__ __align__(1024) unsigned char sm[];
     Fixed &fx = *reinterpret_cast<Fixed *>(sm + kOffFixed);
@@ -960,9 +999,8 @@ __global__ void __launch_bounds__(kNT + 32, 1)
             reinterpret_cast<uint4 *>(sm + kOffB + kBlk)[i] = reinterpret_cast<uint4 *>(sm + kOffC + kBlk)[i] =
                 make_uint4(0u, 0u, 0u, 0u);
     }
-    Piece p;   // the first item's, while tensor memory is allocated
-    int64_t at = blockIdx.x;
-    int z = (int)(at / units);
+    Piece p;   // found while tensor memory is allocated
+    const int z = (int)(blockIdx.x / (unsigned)units);
     bool found = find_cut(a.r, seg, z, p);
     tc_fence_before();
     __syncthreads();
@@ -972,9 +1010,8 @@ __global__ void __launch_bounds__(kNT + 32, 1)
     // (The issuing warp meets the others at the same barriers from code of its own.)
     auto sync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(kNT + 32) : "memory"); };
     int n = 0;   // chunks so far: the barriers' phases
-    for (; at < items; at += gridDim.x, z = (int)(at / units), found = at < items && find_cut(a.r, seg, z, p)) {
-        if (!found) continue;
-        const Unit u = unit_of<HPC>((int)(at - (int64_t)z * units), a.H, a.G);
+    for (; found; found = false) {
+        const Unit u = unit_of<HPC>((int)(blockIdx.x - (unsigned)z * units), a.H, a.G);
         const bool active = hh < u.heads;
         const int t_first = p.j * seg;
         const int tm_t = a.r.cu ? (int)p.row0 : 0, tm_b = a.r.cu ? 0 : p.b;
@@ -1013,6 +1050,7 @@ __global__ void __launch_bounds__(kNT + 32, 1)
                 __syncwarp();
             }
             if (!mbar_wait_bounded(mma_bar, (n - 1) & 1, nullptr)) fx.bad = 1;
+            if (lead && p.row0 + t_first * p.step == a.fail_row) fx.bad = 1;
             sync();   // every wait is over
             sync();   // the state is where X' was
             if (lead) {
@@ -1092,7 +1130,7 @@ __global__ void __launch_bounds__(kNT + 32, 1)
         update_state(S, tl + ((n - 1) & 1) * 128 + cq * CW, keep_before);
         tc_fence_before();
         sync();   // every wait is over
-        const bool bad = fx.bad;   // a wait that ran out leaves no state that looks like one
+        const bool bad = fx.bad;   // after a wait that ran out: NaN
         if (r < DK) {
 #pragma unroll
             for (int i = 0; i < CW / 4; ++i) {
@@ -1163,8 +1201,7 @@ cudaError_t launch(const SsmArgs &a, const SsmMaps &maps, int seg, int tma, int 
     if (split) {
         e = cudaFuncSetAttribute(ssm_state_kernel<DK, HPC>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
-        const int64_t cuts = cut_count(a.r, seg) * units;
-        ssm_state_kernel<DK, HPC><<<grid(cuts), kNT + 32, bytes, s>>>(a, maps, seg, cuts, tma);
+        ssm_state_kernel<DK, HPC><<<(unsigned)(cut_count(a.r, seg) * units), kNT + 32, bytes, s>>>(a, maps, seg, tma);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         e = launch_ssm_join(a, seg, true, s);

@@ -37,7 +37,7 @@ EXPORTED = ["lq_workspace_bytes", "lq_config_check", "lq_state_init", "lq_decode
             "lq_state_destroy", "lq_strerror", "lq_selftest_division", "lq_prefill",
             "lq_state_init_static", "lq_fit_static_scales", "lq_selftest_wait", "lq_state_set_phases",
             "lq_conv_prefill", "lq_conv_step", "lq_ssm_workspace_bytes", "lq_ssm_prefill", "lq_ssm_step",
-            "lq_norm_in", "lq_norm_out"]
+            "lq_norm_in", "lq_norm_out", "lq_selftest_ssm_wait"]
 
 
 class LqError(RuntimeError):
@@ -114,6 +114,8 @@ def lib():
             "lq_ssm_workspace_bytes": (sz, [vp, i32]),
             "lq_ssm_prefill": (C.c_int, [vp, i32, vp, vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, vp, vp, vp, vp, i64,
                                          vp, sz, vp]),
+            "lq_selftest_ssm_wait": (C.c_int, [vp, i32, vp, vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, vp, vp, vp, vp, i64,
+                                               vp, sz, i32, vp]),
             "lq_ssm_step": (C.c_int, [vp, vp, vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, vp, vp, i64, vp]),
             "lq_norm_in": (C.c_int, [vp, vp, i64, vp, vp, i64, vp, vp, i64, vp, i64, vp]),
             "lq_norm_out": (C.c_int, [vp, vp, i64, vp, vp, i64, vp, i64, vp, vp, i64, vp]),
@@ -523,6 +525,23 @@ def lq_ssm_prefill(x, dt, A, Bm, Cm, D=None, dt_bias=None, softplus=True, S0=Non
     (y [..., H, dv], S_out), allocated when None; S_out may be S0.  The
     workspace (uint8, at least lq_ssm_workspace_bytes) is allocated when None."""
     return _call("ssm_prefill", (x, dt, A, Bm, Cm, D, dt_bias, softplus, S0, S_out, y, cu, workspace), stream)
+
+
+def lq_selftest_ssm_wait(row: int, x, dt, A, Bm, Cm, S0, S_out, y, cu=None, workspace=None, stream=None):
+    """lq_ssm_prefill (steps through softplus, no D and bias) of contiguous bf16
+    tensors with a wait of the piece that starts or ends at this row counted as run
+    out: fills y and S_out."""
+    lead, (H, dv), (G, dk) = x.shape[:-2], x.shape[-2:], Bm.shape[-2:]
+    B, rows, bf = S_out.shape[0], lead.numel(), torch.bfloat16
+    cfg = lq_ssm_config(LQ_BF16, B, H, G, dk, dv, 1)
+    off = None if cu is None else _dev(cu, "cu", (B + 1,), torch.int32)
+    px, pdt, py = (_dev(t, n, s, bf) for t, n, s in ((x, "x", x.shape), (dt, "dt", (*lead, H)), (y, "y", x.shape)))
+    pb, pc = (_dev(t, n, (*lead, G, dk), bf) for t, n in ((Bm, "Bm"), (Cm, "Cm")))
+    ps, po = (None if t is None else _dev(t, n, (B, H, dk, dv)) for t, n in ((S0, "S0"), (S_out, "S_out")))
+    ws, n_ws = (None, 0) if workspace is None else (_dev(workspace, "workspace", None, torch.uint8), workspace.numel())
+    _chk(lib().lq_selftest_ssm_wait(C.addressof(cfg), rows, off, px, H * dv, pdt, H, _dev(A, "A", (H,)), pb, G * dk, pc,
+                                    G * dk, None, None, ps, po, py, H * dv, ws, n_ws, row, _stream(stream)),
+         "lq_selftest_ssm_wait")
 
 
 def lq_ssm_step(S, x, dt, A, Bm, Cm, D=None, dt_bias=None, softplus=True, y=None, stream=None):

@@ -93,3 +93,50 @@ def test_packed_prompts_cut_in_some_sequences_at_odd_bases(dtype):
     assert (got[:9] == 7).all() and (got[2046:] == 7).all()
     _close(got[9:2046], want, ty, f"ssm cut at odd bases {ids(dtype)} y")
     _close(S, rS, tS, f"ssm cut at odd bases {ids(dtype)} S")
+
+
+@pytest.mark.parametrize("H,G,dk,dv,lens,B,row,nan", [
+    # 12 pieces of 128 tokens; the fourth one's start: also its own state, so all behind it
+    (3, 1, 64, 64, [1500], 1, 384, [(384, 1500)]),
+    (3, 1, 64, 64, [1500], 1, 511, [(384, 512)]),          # its end: the scan of that piece alone
+    (2, 1, 128, 128, [1500], 1, 1499, [(1408, 1500)]),     # the last piece's end: the state too
+    (2, 1, 128, 128, None, 2, 257, [(128, 1100)]),         # time-major, cut: token 128 of sequence 1
+    # walked: and what the same CTAs take afterwards
+    (9, 1, 128, 128, [200, 140, 0, 131] * 9, 36, 200, None),
+    (9, 1, 128, 128, [200, 140, 0, 131] * 9, 36, 339, None),
+    (9, 1, 128, 128, [200, 140, 0, 131] * 9, 36, 9 * 471 - 1, None),
+    (8, 2, 64, 64, [300, 7] * 30, 60, 614, None),
+], ids=["piece_start", "piece_end", "last_end", "time_major_cut", "start", "end", "very_last", "cut_and_walked"])
+def test_a_wait_that_runs_out_leaves_nan(H, G, dk, dv, lens, B, row, nan):
+    """A wait counted as run out (lq_selftest_ssm_wait; every real wait ends):
+    the outputs and states behind it are NaN, every other value is that of the
+    ordinary call, and nothing keeps what its memory held before."""
+    _gpu()
+    lead = (1100, B) if lens is None else (sum(lens),)
+    cu = None if lens is None else _cu(lens)
+    v = {k: t.contiguous() for k, t in _ssm_inputs(90 + H, lead, B, H, G, dk, dv, BF16).items()}
+    args = [v[k] for k in ("x", "dt", "A", "Bm", "Cm")]
+    want, wS = lq.lq_ssm_prefill(*args, S0=v["S0"], cu=cu)
+    n_ws = lq.lq_ssm_workspace_bytes(BF16, B, H, G, dk, dv, want[..., 0, 0].numel())
+    ws = torch.full((n_ws,), 1, dtype=torch.uint8, device="cuda") if n_ws else None
+    y, S = torch.full_like(want, 7.0), torch.full_like(wS, 7.0)
+    lq.lq_selftest_ssm_wait(row, *args, v["S0"], S, y, cu=cu, workspace=ws)
+    for got, ref in ((y, want), (S, wS)):
+        off = torch.isnan(got)
+        assert (off | (got == ref)).all()
+        # whole heads of a row, whole states
+        assert torch.equal(off.any(-1), off.all(-1))
+    assert torch.equal(torch.isnan(S).flatten(2).any(-1), torch.isnan(S).flatten(2).all(-1))
+    b = row % B if lens is None else int((cu > row).nonzero()[0]) - 1
+    mine = y[:, b] if lens is None else y[int(cu[b]):int(cu[b + 1])]
+    bad = torch.isnan(mine).all(-1).all(-1)
+    if nan is None:
+        at = row if lens is None else row - int(cu[b])
+        assert bad[at:].all() and torch.isnan(S[b]).all()
+    else:
+        assert [(int(i.min()), int(i.max()) + 1) for i in [bad.nonzero()]] == nan and bad.sum() == nan[0][1] - nan[0][0]
+        assert torch.isnan(S[b]).all() if nan[0][1] == mine.shape[0] else not torch.isnan(S).any()
+        assert torch.isnan(y).sum() == bad.sum() * H * dv
+    # an ordinary call afterwards is as before
+    again, aS = lq.lq_ssm_prefill(*args, S0=v["S0"], cu=cu)
+    assert torch.equal(again, want) and torch.equal(aS, wS)
