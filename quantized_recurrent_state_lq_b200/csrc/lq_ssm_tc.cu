@@ -30,11 +30,12 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
 }
 
 // x = big + small, both rounded to TF32 (nearest, by adding half a unit to the
-// bits): within 2^-22 of x.  A NaN stays one in big (the addition would carry it
-// into the sign), an infinity too; small is whatever it is beside those.
+// bits): within 2^-22 of x.  Where that would pass the largest TF32 value (the last
+// 2^-11 of the FP32 range) big is cut instead and small takes what is left; an
+// infinity or a NaN is not finite in big, and small is whatever it is beside it.
 __device__ __forceinline__ void split(float x, uint32_t &big, uint32_t &small) {
     const uint32_t u = __float_as_uint(x);
-    big = x == x ? (u + 0x1000u) & 0xffffe000u : u;
+    big = (fabsf(x) < __int_as_float(0x7f7ff000) ? u + 0x1000u : u) & 0xffffe000u;
     small = (__float_as_uint(x - __uint_as_float(big)) + 0x1000u) & 0xffffe000u;
 }
 

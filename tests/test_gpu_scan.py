@@ -5,7 +5,7 @@ import torch
 
 from quantized_recurrent_state_lq_b200 import lq
 from tests import layer_ref as R
-from tests.test_gpu_layer import BF16, F16, TYPES, _check_ssm, _close, _cu, _gpu, _ssm_inputs, _ssm_tol, ids
+from tests.test_gpu_layer import BF16, F16, F32, TYPES, _check_ssm, _close, _cu, _gpu, _ssm_inputs, _ssm_tol, ids
 
 pytestmark = pytest.mark.gpu
 
@@ -140,3 +140,36 @@ def test_a_wait_that_runs_out_leaves_nan(H, G, dk, dv, lens, B, row, nan):
     # an ordinary call afterwards is as before
     again, aS = lq.lq_ssm_prefill(*args, S0=v["S0"], cu=cu)
     assert torch.equal(again, want) and torch.equal(aS, wS)
+
+
+@pytest.mark.parametrize("dtype", [F32], ids=ids)
+def test_states_at_the_end_of_the_fp32_range(dtype):
+    """States within 2^-13 of the FP32 maximum that C reads at 2^-70: every
+    output is far inside the range, though rounding the state itself to fewer
+    bits would pass the end of it."""
+    _gpu()
+    v = _ssm_inputs(97, (70,), 1, 4, 1, 64, 64, dtype)
+    big = torch.finfo(F32).max * (1 - 2.0 ** -14)
+    v["S0"] = torch.where(v["S0"] < 0, -big, big)
+    v["Cm"] = (v["Cm"].float() * 2.0 ** -70).to(dtype)
+    v["A"] = torch.tensor([-2.0 ** -20, -0.01, -1.0, -16.0], device="cuda")
+    v["dt"] = (v["dt"].abs() * 0.01).to(dtype)
+    v["D"] = v["dt_bias"] = None
+    _check_ssm(v, _cu([70]), f"ssm end of the range {ids(dtype)}", softplus=False)
+
+
+@pytest.mark.parametrize("dtype", [F32], ids=ids)
+def test_values_at_the_end_of_the_fp32_range(dtype):
+    """x at the type's largest values beside steps of 1 (bf16: 1.003, within the
+    FP32 range but past the end of bf16's) and B and C at 2^-40."""
+    _gpu()
+    v = _ssm_inputs(98, (70,), 1, 2, 1, 64, 64, dtype)
+    big = torch.finfo(dtype).max if dtype == BF16 else torch.finfo(F32).max * (1 - 2.0 ** -14)
+    v["x"] = torch.where(v["x"] < 0, -big, big).to(dtype)
+    v["Bm"], v["Cm"] = ((v[k].float() * 2.0 ** -40).to(dtype) for k in ("Bm", "Cm"))
+    v["dt"] = torch.full_like(v["dt"], 1.0)
+    v["dt_bias"] = torch.full((2,), 0.003 if dtype == BF16 else 0.0, device="cuda")
+    v["A"] = torch.tensor([-1e-6, -0.5], device="cuda")
+    v["D"] = torch.tensor([0.5, 2.0 ** -30], device="cuda")
+    v["S0"] = None
+    _check_ssm(v, _cu([70]), f"ssm values at the end of the range {ids(dtype)}", softplus=False)
