@@ -140,8 +140,11 @@ __device__ __forceinline__ uint32_t last_part(float2 v) {
     const __nv_bfloat162 p = __floats2bfloat162_rn(v.x, v.y);
     return *reinterpret_cast<const uint32_t *>(&p);
 }
+// (Values past the largest bf16 become that: the rest holds what is left of them,
+// an infinity too.)
 __device__ __forceinline__ uint32_t take_part(float2 &v) {
-    const uint32_t w = last_part(v);
+    uint32_t w;
+    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(v.y), "f"(v.x));
     v = ffma2(bf16x2_to_f2(w), f2(-1.0f, -1.0f), v);
     return w;
 }

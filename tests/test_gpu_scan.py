@@ -142,7 +142,7 @@ def test_a_wait_that_runs_out_leaves_nan(H, G, dk, dv, lens, B, row, nan):
     assert torch.equal(again, want) and torch.equal(aS, wS)
 
 
-@pytest.mark.parametrize("dtype", [F32], ids=ids)
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=ids)
 def test_states_at_the_end_of_the_fp32_range(dtype):
     """States within 2^-13 of the FP32 maximum that C reads at 2^-70: every
     output is far inside the range, though rounding the state itself to fewer
@@ -158,7 +158,7 @@ def test_states_at_the_end_of_the_fp32_range(dtype):
     _check_ssm(v, _cu([70]), f"ssm end of the range {ids(dtype)}", softplus=False)
 
 
-@pytest.mark.parametrize("dtype", [F32], ids=ids)
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=ids)
 def test_values_at_the_end_of_the_fp32_range(dtype):
     """x at the type's largest values beside steps of 1 (bf16: 1.003, within the
     FP32 range but past the end of bf16's) and B and C at 2^-40."""
