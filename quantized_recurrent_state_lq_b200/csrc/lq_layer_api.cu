@@ -186,10 +186,10 @@ int ssm_prefill(const lq_ssm_config *cfg, int32_t rows, const int32_t *d_cu, con
         const int64_t sb = (int64_t)cfg->B * cfg->H * cfg->dk * cfg->dv * 4;
         const Span ws = flat(d_ws, (int64_t)need);
         const Span other[] = {rows_of(d_x, rows, wx, ldx, e),  rows_of(d_dt, rows, cfg->H, lddt, e),
-                           rows_of(d_Bm, rows, wb, ldb, e), rows_of(d_Cm, rows, wb, ldc, e),
-                           rows_of(d_y, rows, wx, ldy, e),  flat(d_S0, sb), flat(d_S_out, sb),
-                           flat(d_A, (int64_t)cfg->H * 4),  flat(d_D, (int64_t)cfg->H * 4),
-                           flat(d_dt_bias, (int64_t)cfg->H * 4), offsets(a.r)};
+                              rows_of(d_Bm, rows, wb, ldb, e), rows_of(d_Cm, rows, wb, ldc, e),
+                              rows_of(d_y, rows, wx, ldy, e),  flat(d_S0, sb), flat(d_S_out, sb),
+                              flat(d_A, (int64_t)cfg->H * 4),  flat(d_D, (int64_t)cfg->H * 4),
+                              flat(d_dt_bias, (int64_t)cfg->H * 4), offsets(a.r)};
         for (const Span &o : other)
             if (overlap(ws, o)) return LQ_ERR_INVALID_ARG;
         a.ws = static_cast<float *>(d_ws);
