@@ -3,7 +3,9 @@
 nvcc compiles every csrc/*.cu for sm_100a only and links them, with the CUDA
 runtime linked statically, into quantized_recurrent_state_lq_b200/liblq.so;
 g++ compiles csrc/lq_bind.cpp (host code, against torch) into _bind.so beside it.
-Run `python -m quantized_recurrent_state_lq_b200.build` or call build().
+Run `python -m quantized_recurrent_state_lq_b200.build` or call build() and
+build_bind(); the binding is built where its calls are first made if it is
+missing, the library alone needs no host compiler for torch's headers.
 """
 from __future__ import annotations
 
@@ -70,8 +72,6 @@ def build_bind(verbose: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
-    if force or bind_stale():
-        build_bind(verbose)
     if not force and not _stale():
         return OUT
     objs = []
@@ -98,4 +98,6 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
 if __name__ == "__main__":
     build(force="--force" in sys.argv, verbose=True,
           extra=["-Xptxas", "-v"] if "--ptxas" in sys.argv else None)
+    if "--force" in sys.argv or bind_stale():
+        build_bind(verbose=True)
     print(OUT)

@@ -80,8 +80,6 @@ def lib():
         from . import build as _build
         if not os.path.exists(LIB_PATH) or _build._stale():
             _build.build()
-        elif _build.bind_stale():
-            _build.build_bind()
         L = C.CDLL(LIB_PATH)
         vp, i32, i64, sz = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t
         cfgp = C.POINTER(lq_config)
@@ -467,6 +465,9 @@ def _binding():
     global _native
     if _native is None:
         L = lib()
+        from . import build as _build
+        if _build.bind_stale():
+            _build.build_bind()
         from . import _bind
         _bind.load(*(C.cast(getattr(L, n), C.c_void_p).value for n in _BOUND))
         _native = _bind
