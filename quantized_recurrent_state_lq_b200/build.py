@@ -2,7 +2,8 @@
 
 nvcc compiles every csrc/*.cu for sm_100a only and links them, with the CUDA
 runtime linked statically, into quantized_recurrent_state_lq_b200/liblq.so;
-g++ compiles csrc/lq_bind.cpp (host code, against torch) into _bind.so beside it.
+g++ compiles csrc/lq_bind.cpp (host code, against torch) into _bind.<Python>.<torch>.so
+beside it.
 Run `python -m quantized_recurrent_state_lq_b200.build` or call build() and
 build_bind(); the binding is built where its calls are first made if it is
 missing, the library alone needs no host compiler for torch's headers.
@@ -20,7 +21,6 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "liblq.so")
 BIND_SRC = os.path.join(CSRC, "lq_bind.cpp")
-BIND_OUT = os.path.join(HERE, "_bind.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -41,11 +41,22 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def bind_path() -> str:
+    """The binding for this Python and this torch: both are named in the file,
+    since one compiled against another's headers may load and misread tensors."""
+    import sysconfig
+
+    import torch
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    return os.path.join(HERE, f"_bind.{sysconfig.get_config_var('SOABI')}.torch-{torch.__version__}-abi{abi}.so")
+
+
 def bind_stale() -> bool:
-    if not os.path.exists(BIND_OUT):
+    out = bind_path()
+    if not os.path.exists(out):
         return True
     deps = [BIND_SRC, os.path.join(ROOT, "include", "lq_state.h")]
-    return any(os.path.getmtime(d) > os.path.getmtime(BIND_OUT) for d in deps)
+    return any(os.path.getmtime(d) > os.path.getmtime(out) for d in deps)
 
 
 def _bind_command(out: str) -> list[str]:
@@ -63,12 +74,13 @@ def _bind_command(out: str) -> list[str]:
 
 
 def build_bind(verbose: bool = False) -> str:
-    cmd = _bind_command(BIND_OUT + ".tmp")
+    out = bind_path()
+    cmd = _bind_command(out + ".tmp")
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
-    os.replace(BIND_OUT + ".tmp", BIND_OUT)
-    return BIND_OUT
+    os.replace(out + ".tmp", out)
+    return out
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:

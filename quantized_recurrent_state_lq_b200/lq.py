@@ -9,6 +9,7 @@ raises on import of the library instead of falling back.
 from __future__ import annotations
 
 import ctypes as C
+import importlib.util
 import os
 from dataclasses import dataclass
 
@@ -468,9 +469,11 @@ def _binding():
         from . import build as _build
         if _build.bind_stale():
             _build.build_bind()
-        from . import _bind
-        _bind.load(*(C.cast(getattr(L, n), C.c_void_p).value for n in _BOUND))
-        _native = _bind
+        spec = importlib.util.spec_from_file_location("_bind", _build.bind_path())
+        bind = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(bind)
+        bind.load(*(C.cast(getattr(L, n), C.c_void_p).value for n in _BOUND))
+        _native = bind
     return _native
 
 

@@ -19,3 +19,22 @@ def test_the_library_loads_without_the_binding(monkeypatch):
     assert build.build() == build.OUT
     with pytest.raises(FileNotFoundError):      # and the calls that need it say so
         lq._binding()
+
+
+def test_a_binding_of_another_torch_or_python_is_not_taken(monkeypatch):
+    """The binding holds the layouts of the torch and Python it was compiled
+    against: under another of either it counts as missing."""
+    import sysconfig
+
+    import torch
+    if build.bind_stale():
+        build.build_bind()
+    here = build.bind_path()
+    assert not build.bind_stale()
+    monkeypatch.setattr(torch, "__version__", torch.__version__ + ".other")
+    assert build.bind_stale() and build.bind_path() != here
+    monkeypatch.undo()
+    assert not build.bind_stale()
+    var = sysconfig.get_config_var
+    monkeypatch.setattr(sysconfig, "get_config_var", lambda n: "cpython-399" if n == "SOABI" else var(n))
+    assert build.bind_stale() and build.bind_path() != here
