@@ -15,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -74,12 +75,21 @@ def _bind_command(out: str) -> list[str]:
 
 
 def build_bind(verbose: bool = False) -> str:
+    """Compiles into a file of this call's own, so that ranks that build at the
+    same time each put a whole one in place."""
     out = bind_path()
-    cmd = _bind_command(out + ".tmp")
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
-    os.replace(out + ".tmp", out)
+    fd, tmp = tempfile.mkstemp(prefix="_bind.", suffix=".tmp.so", dir=HERE)
+    os.close(fd)
+    try:
+        cmd = _bind_command(tmp)
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+        os.chmod(tmp, 0o755)
+        os.replace(tmp, out)
+    except BaseException:
+        os.unlink(tmp)
+        raise
     return out
 
 

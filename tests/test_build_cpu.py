@@ -38,3 +38,28 @@ def test_a_binding_of_another_torch_or_python_is_not_taken(monkeypatch):
     var = sysconfig.get_config_var
     monkeypatch.setattr(sysconfig, "get_config_var", lambda n: "cpython-399" if n == "SOABI" else var(n))
     assert build.bind_stale() and build.bind_path() != here
+
+
+def test_builds_at_the_same_time_do_not_share_a_file(monkeypatch, tmp_path):
+    """Two builds of the binding, the second while the first one's compiler is
+    still at work: each writes a file of its own and puts it in place whole; a
+    compiler that fails leaves nothing behind."""
+    monkeypatch.setattr(build, "HERE", str(tmp_path))
+    written = []
+
+    def compiler(cmd, check):
+        out = cmd[cmd.index("-o") + 1]
+        written.append(out)
+        if len(written) == 1:
+            build.build_bind()
+        if len(written) == 3:
+            raise RuntimeError("compiler failed")
+        with open(out, "w") as f:
+            f.write("library %d" % written.index(out))
+    monkeypatch.setattr(build.subprocess, "run", compiler)
+    path = build.build_bind()
+    assert len(set(written)) == 2 and path not in written
+    assert open(path).read() == "library 0"
+    with pytest.raises(RuntimeError):
+        build.build_bind()
+    assert [str(p) for p in tmp_path.iterdir()] == [path]
