@@ -231,19 +231,20 @@ class ScanRunner:
     def capture(self):
         """A CUDA graph of one step on fixed buffers: fill x_in (and res_in), call
         replay(), read the returned (out, residual)."""
-        keep = self.window.clone(), self.state.clone()
-        self.x_in = torch.zeros((self.B, self.sl.d), dtype=self.dtype, device=self.window.device)
-        self.res_in = torch.zeros_like(self.x_in)
-        s = torch.cuda.Stream()
-        s.wait_stream(torch.cuda.current_stream())
-        with torch.cuda.stream(s):
-            self.step(self.x_in, self.res_in)      # warm the launch path before capture
-        torch.cuda.current_stream().wait_stream(s)
-        self.graph = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(self.graph):
-            self.out = self.step(self.x_in, self.res_in)
-        self.window.copy_(keep[0])
-        self.state.copy_(keep[1])
+        with torch.cuda.device(self.window.device):   # its streams are the current device's otherwise
+            keep = self.window.clone(), self.state.clone()
+            self.x_in = torch.zeros((self.B, self.sl.d), dtype=self.dtype, device=self.window.device)
+            self.res_in = torch.zeros_like(self.x_in)
+            s = torch.cuda.Stream()
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                self.step(self.x_in, self.res_in)      # warm the launch path before capture
+            torch.cuda.current_stream().wait_stream(s)
+            self.graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(self.graph):
+                self.out = self.step(self.x_in, self.res_in)
+            self.window.copy_(keep[0])
+            self.state.copy_(keep[1])
 
     def replay(self):
         self.graph.replay()
