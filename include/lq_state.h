@@ -423,7 +423,9 @@ size_t lq_ssm_workspace_bytes(const lq_ssm_config *cfg, int32_t rows);
  * cores: the state with FP32-level accuracy, the outputs within 2^-17 of their
  * terms for bf16 (two-part operands; one rounding to bf16 is 2^-9; 2^-16 of a term
  * that has decayed below 2^-64) and FP32-level for f32 and f16.  One step's decay exp(d_t A_h) is kept within 2^-150 .. 2^150
- * there (beyond, FP32 has 0 and infinity).  A value of x, Bm, Cm or dt that is not
+ * there (beyond, FP32 has 0 and infinity); where steps make a state grow by 2^127
+ * and more within 128 tokens, infinities and NaN may come earlier than token by
+ * token.  A value of x, Bm, Cm or dt that is not
  * finite shows in the outputs and states it reaches and in no earlier token; where
  * it reaches a state's column or row, those entries are not finite (NaN or
  * infinite).  A call gives the same bits every time.  Every wait inside has a time

@@ -8,11 +8,11 @@
 // kRun tokens of one sequence for 4 channels (one for widths or rows whose
 // alignment does not allow that): 4 channels keep a warp's accesses whole lines
 // at 4 K weights in registers, half the registers and twice the warps of 8
-// channels (119 us against 65 us for 32768 x 2304 bf16).  The next kAhead rows
+// channels (119 us against 66 us for 32768 x 2304 bf16).  The next kAhead rows
 // are on their way while one batch is at work, and the K-1 inputs behind stay
 // in registers, so an input is read once plus K-1 halo rows per run.  Sums are
 // FP32, the output is rounded once; the window holds the inputs as they came.
-// 65 us is 0.72 of the copy rate: instruction issue (62% of slots, the exponential
+// 66 us is 0.70 of the copy rate: instruction issue (62% of slots, the exponential
 // and reciprocal of two channels at a time the largest part) beside the loads.
 #include "lq_act.cuh"
 #include "lq_common.cuh"

@@ -10,8 +10,8 @@
 // when rows and strides are 16-byte aligned, else one.  Every element is read
 // by the thread that writes it, after the whole group has been read, so y and
 // h may be x, z or res themselves.  norm_in of 16384 rows of 4096 bf16 (537 MB):
-// 85 us, 0.97 of the copy rate; norm_out of 16384 rows of 2048 f16 with gate and
-// residual (268 MB): 50 us, 0.83 (issue at 76%, the gates' exponentials).
+// 89 us, 0.92 of the copy rate; norm_out of 16384 rows of 2048 f16 with gate and
+// residual (268 MB): 53 us, 0.77 (issue at 76%, the gates' exponentials).
 #include "lq_act.cuh"
 
 namespace lq {
@@ -155,8 +155,10 @@ cudaError_t launch(const NormArgs &a, cudaStream_t s) {
 // that most of them have work, few enough elements (up to 64 in registers) that
 // small groups do not step through empty ones.  Without vector accesses the time
 // goes to latency with every warp an SM holds at work, so what counts is the
-// groups in flight: small teams of 4 to 12 elements a thread (16.8 M elements of bf16
-// norm_in, groups of 31: 14 us, 29 with a warp each; 130: 13 and 30; 1025: 13 and 23).
+// groups in flight: small teams of 4 to 12 elements a thread (norm_in of 67 M bf16
+// elements, 537 MB in its four arrays, groups of 31: 184 us, 437 with a warp each; of
+// 130: 163 and 438; of 1025: 159 and 328; a sixteenth of that, within L2: 14 and 29,
+// 12 and 29, 12 and 23).
 template <typename T, typename TX, bool IN>
 cudaError_t by_size(const NormArgs &a, cudaStream_t s) {
     const uintptr_t base = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.z) |

@@ -10,7 +10,7 @@
 // the GPU (16 16-byte loads in flight per thread), 16 when they do not (four
 // times the CTAs, a quarter of the serial work each).  The state stays in
 // registers over the tokens of a short prompt.  256 sequences of 32 heads of
-// 128 x 128 (1.07 GB): 163 us, the copy rate.
+// 128 x 128 (1.07 GB): 161 us, the copy rate.
 #include <algorithm>
 
 #include "lq_ssm.h"
@@ -141,7 +141,7 @@ constexpr int kJoin = 8, kJoinThreads = 128;
 
 // One thread per 4 state elements; block y takes every gridDim.y-th sequence and
 // skips those of one piece, 32 at a time.  kJoin pieces' states are on their way
-// at a time (128 pieces of 2 heads of 64 x 64: 37 us for the prompt, 62 one by one).
+// at a time (128 pieces of 2 heads of 64 x 64: 25 us less than one by one, of 62).
 __global__ void __launch_bounds__(kJoinThreads) ssm_join_kernel(SsmArgs a, int seg, bool early) {
     const int64_t per = (int64_t)a.dk * a.dv / 4, all = per * a.H;
     const int64_t i = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x;   // (head, element)
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kJoinThreads) ssm_join_kernel(SsmArgs a, int s
 
 // What runs side by side: for bf16 one CTA per SM and 128 value columns, else a
 // head each, two per SM for 128 value columns and four for 64 (16384 tokens of 16
-// heads of 64 x 64: 273 us against 407 with two).
+// heads of 64 x 64: 267 us against 407 with two).
 struct Fit {
     int64_t units, slots, chunk;
     Fit(int dtype, int H, int G, int dv) : units(H), slots(dv == 64 ? 148 * 4 : 148 * 2), chunk(32) {
@@ -209,9 +209,9 @@ int ragged_piece(const Fit &f, int64_t rows) {
 // costs two launches and the pieces' own states at a third (by mma.sync 0.45) of a
 // chunk's time.  bf16: not cut, or in as many pieces as give each CTA one, or one more
 // or half as many; more pieces than CTAs leave some CTAs with part of a piece more
-// than their share.  (16000 tokens of 10 sequences, 8 heads of 128 x 128: 90 us uncut,
+// than their share.  (16000 tokens of 10 sequences, 8 heads of 128 x 128: 95 us uncut,
 // 128 cut.)  f32, f16: not cut, or as above -- several CTAs share an SM, whose rate is
-// what counts.  (3000 tokens of 20 sequences, 24 f32 heads of 64 x 64: 65 and 107 us.)
+// what counts.  (3000 tokens of 20 sequences, 24 f32 heads of 64 x 64: 67 and 107 us.)
 int even_piece(const Fit &f, int dtype, int64_t B, int64_t T) {
     const int64_t n = (T + f.chunk - 1) / f.chunk, all = B * f.units;
     if (dtype != kBF16) {
@@ -256,7 +256,7 @@ cudaError_t launch_ssm_join(const SsmArgs &a, int seg, bool early, cudaStream_t 
 // bf16, 9 for f16, 14 for f32) whatever it holds, a token 0.35 us with fewer CTAs
 // than SMs and 0.6 with more: so do sequences of at most 16 tokens, 24 of few heads
 // (f16 chunks are of 32), and packed batches of at most 2 tokens a sequence on
-// average and 512 in all (64 single tokens of 32 heads of 128 x 128: 50 us against
+// average and 512 in all (64 single tokens of 32 heads of 128 x 128: 45 us against
 // 155), where one long sequence costs no more than 512 steps.
 bool token_by_token(const SsmArgs &a, int dtype) {
     const Rows &r = a.r;

@@ -14,7 +14,7 @@
 // Bound: with few CTAs latency (a chunk of a 64 x 64 head 10000 cycles, f32: rows
 // 2000, G 2600, C S 1900, M X and the state 2700), with many the rate of mma.sync:
 // two CTAs per SM for 128 value columns, four for 64.  3001 f16 tokens of 6 heads
-// of 64 x 128: 37 us; 16384 f32 tokens of 16 heads of 128 x 128: 832 us.
+// of 64 x 128: 35 us; 16384 f32 tokens of 16 heads of 128 x 128: 840 us.
 #include "lq_ssm.h"
 
 namespace lq {
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(2 * DV, DV == 128 ? 2 : 4) ssm_tc_kernel(SsmAr
         float Y[Q / 8][4] = {};   // Y^T tile j: value columns pc + gq (+8), tokens 8 j + 2 tq (+1)
         if (FULL) {
             // (All token blocks in one pass over S: taken two at a time, S's parts are
-            // kept for the second pass and spill, 944 us against 832 for 16384 tokens of
+            // kept for the second pass and spill, 944 us against 840 for 16384 tokens of
             // 16 f32 heads of 128 x 128.)
             float alt[Q / 8][4] = {}, low[Q / 8][4] = {};
 #pragma unroll

@@ -25,9 +25,9 @@
 // Long sequences of a small batch are cut into pieces: ssm_state_kernel forms each
 // piece's own state, ssm_join_kernel chains them, and the scan starts every piece
 // from its state (about a third more work for as many times the parallelism).
-// 16384 rows of 40 sequences, 32 heads of 128 x 128: 290 us, tensor work 40% of a
+// 16384 rows of 40 sequences, 32 heads of 128 x 128: 300 us, tensor work 40% of a
 // chunk's 11400 cycles and shared memory at work for 58% of them; one prompt of 16384,
-// 32 heads of 128 x 64: 178 us (the pieces' states 42 of it, their join 6).
+// 32 heads of 128 x 64: 185 us (the pieces' states 42 of it, their join 6).
 //
 // Shared memory holds every operand as rows of 64 columns (128 bytes, the
 // 16-byte chunks XOR-swizzled by the row's low 3 bits) in blocks of 16 KB:

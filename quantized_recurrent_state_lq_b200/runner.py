@@ -182,8 +182,8 @@ def scan_weights(sl: ScanLayer, dtype=torch.bfloat16, device="cuda") -> dict:
 class ScanRunner:
     """One selective-scan layer for a batch of B sequences, prompts and single
     tokens: norm with the residual (lq_norm_in), input projection, short
-    convolution (lq_conv_*), scan (lq_ssm_*), gated norm per head (lq_norm_out),
-    output projection.  The projections are plain library products; all else
+    convolution (lq_conv_*), scan (lq_ssm_*), norm of each head's outputs and then
+    the gate (lq_norm_out), output projection.  The projections are plain library products; all else
     runs in liblq.so.  Holds the sequences' convolution windows and states."""
 
     def __init__(self, sl: ScanLayer, B: int, dtype=torch.bfloat16, device="cuda", weights=None):
@@ -207,7 +207,8 @@ class ScanRunner:
     def prompt(self, x: torch.Tensor, res=None, cu=None):
         """Tokens of all sequences, x [rows, d] with cu or [T, B, d], from the
         windows and states held, which move on.  Returns (block output,
-        residual): the next block's norm adds them."""
+        residual): the next block's norm adds them.  Output rows of no sequence
+        (before cu[0], from cu[B] on) hold nothing in particular."""
         sl, w = self.sl, self.w
         u, h = lq.lq_norm_in(x, w["w_norm"], res=res, scale=sl.scale, eps=sl.eps)
         z, xbc, dt = self._split(u @ w["w_in"])
